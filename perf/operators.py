@@ -266,7 +266,7 @@ def _plain_page_plan(s):
     cum = grow.cumsum(0)
     ok = (grow == 0) | (cum <= count)
     granted = torch.where(ok, new, 0)
-    taken = torch.where(ok, cum, 0).amax()
+    taken = torch.where(cum <= count, cum, 0).amax()
     now = torch.where(ok, need, held)
     col = torch.arange(P, device=ctx.device)[None, :]
     fresh = (col >= held[:, None]) & (col < now[:, None])
