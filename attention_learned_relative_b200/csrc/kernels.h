@@ -142,4 +142,77 @@ cudaError_t launch_decode_bf16(const CUtensorMap& tk, const CUtensorMap& tv, con
 cudaError_t launch_decode_paged_bf16(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
                                      cudaStream_t stream);
 
+// Largest drafted tree, and largest accepted path (paged_ops.cu, tree_sm100.cu).
+constexpr int kMaxTree = 128;
+
+// Operators around the paged cache (paged_ops.cu).
+struct PagePlanParams {
+    const int* ctx_lens;     // [B] rows already in the cache
+    const int* new_lens;     // [B] rows to add, at most T
+    const int* num_blocks;   // [B] pages each request holds
+    int* num_blocks_out;     // [B]
+    int* block_table;        // [B, max_pages], updated in place
+    int* free_ring;          // [num_pages], updated in place
+    const int* ring_state;   // {head, count}
+    int* ring_state_out;
+    int* granted;            // [B]
+    int* slots;              // [B, T]
+    int B, T, page_size, max_pages, num_pages;
+};
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream);
+
+struct TreePlanParams {
+    const int* parents;      // [B, T]
+    const int* lens;         // [B]
+    int* depth;              // [B, T]
+    int* mask;               // [B, T, ceil(T / 32)]
+    int B, T;
+};
+cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream);
+
+struct KvAppendParams {
+    const void *q, *k, *v;   // rows of heads_q / Hkv / Hkv heads; strides in elements between tokens
+    long long q_stride, k_stride, v_stride;
+    const int* slots;        // [ntok] cache row, or < 0 for padding
+    const float *q_weight, *k_weight;   // [d], or nullptr: no norm
+    void* q_out;             // [ntok, heads_q, d]
+    void *k_pages, *v_pages; // [num_slots, Hkv, d]
+    int ntok, heads_q, Hkv;  // heads_q = 0: no queries
+    int num_slots;           // num_pages * page_size
+    float eps;
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, int d, cudaStream_t stream);
+
+struct KvCompactParams {
+    void *k_pages, *v_pages; // [layers, num_pages, page_size, row_vecs] 16-byte vectors
+    const int* block_table;  // [B, max_pages]
+    const int* ctx_lens;     // [B]
+    const int* path;         // [B, A]
+    const int* path_lens;    // [B]
+    int B, A, layers, num_pages, page_size, max_pages, row_vecs;
+};
+cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream);
+
+// Attention of drafted trees over a paged cache (tree_sm100.cu).
+struct TreeAttnParams {
+    const __nv_bfloat16* q;          // [B, T, Hq, d]
+    const __nv_bfloat16 *k_pages, *v_pages;
+    const int* block_table;          // [B, max_pages]
+    const int* ctx_lens;             // [B] rows of the prefix
+    const int* tree_lens;            // [B] nodes of the tree
+    const int* depth;                // [B, T]
+    const int* mask;                 // [B, T, words]
+    const float* r;                  // [B, T, Hq]
+    const float* w;                  // [Hq, R]
+    __nv_bfloat16* o;                // [B, T, Hq, d]
+    float* lse;                      // [B, Hq, T] or nullptr
+    int B, T, Hq, Hkv, G, words;
+    int num_pages, page_size, max_pages, max_ctx;
+    int window, R;
+    float scale_log2, inv_scale;
+    int temp_n0;
+    float inv_log_n0;
+};
+cudaError_t launch_tree_attn(const TreeAttnParams& p, int d, cudaStream_t stream);
+
 }  // namespace relbias

@@ -1,0 +1,448 @@
+// paged_ops.cu -- the operators around a paged key/value cache that a serving step
+// needs besides attention: block tables and slot maps built on the GPU from request
+// lengths (page_plan), the write of new K and V rows into their pages with the
+// per-head norm of queries and keys (kv_append), the plan of drafted token trees
+// (tree_plan), and the move of an accepted path's rows to the rows they will keep
+// (kv_compact).  The paged cache and its variable lengths are those the essay
+// "Thinking Machines dropped RoPE" names in its closing section on kernel cost; the
+// per-head norm of queries and keys is the one its logit-scaling paragraph reasons
+// about.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace relbias {
+
+namespace {
+
+// ------------------------------------------------------------------ page_plan
+//
+// need_b  = ceil((ctx_b + new_b) / page)       pages request b will hold
+// grow_b  = max(0, need_b - held_b),  shrink_b = max(0, held_b - need_b)
+// cum_b   = grow_0 + ... + grow_b;  request b is granted iff grow_b = 0 or cum_b <= count
+// The free pages are a ring of N entries, `count` of them valid from `head` on.  Request
+// b's i-th new page is ring[head + cum_b - grow_b + i]; its i-th returned page goes to
+// ring[head + count + (shrink_0 + ... + shrink_(b-1)) + i].  All returned and remaining
+// pages are distinct, so the entries read and the entries written never meet, and no
+// block waits for another: each block sums the demands of the requests before its own
+// (B ints from L2) and the whole plan is one launch.
+//
+// Bounded by the launch and two dependent L2 round trips for small batches, and by the
+// slot map's stores for long prompts.
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanSlots = 8 * kPlanThreads;   // slots a block writes
+
+struct Demand {
+    int grow, shrink, need, granted;
+};
+
+// Pages request b asks for; a request whose numbers are out of range asks for none.
+__device__ __forceinline__ Demand plan_demand(const PagePlanParams& p, int b, bool& bad) {
+    const int ctx = __ldg(p.ctx_lens + b), add = __ldg(p.new_lens + b), held = __ldg(p.num_blocks + b);
+    Demand d{0, 0, held, 0};
+    bad = ctx < 0 || add < 0 || add > p.T || held < 0 || held > p.max_pages;
+    if (!bad) {
+        const long long rows = static_cast<long long>(ctx) + add;
+        if (rows > static_cast<long long>(p.max_pages) * p.page_size) {
+            bad = true;
+        } else {
+            d.need = static_cast<int>((rows + p.page_size - 1) / p.page_size);
+            d.grow = max(0, d.need - held);
+            d.shrink = max(0, held - d.need);
+            d.granted = add;
+        }
+    }
+    return d;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Entry `at` (>= 0) of the ring.
+__device__ __forceinline__ int ring_index(const PagePlanParams& p, long long at) {
+    return static_cast<int>(at % p.num_pages);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanParams p) {
+    __shared__ long long part[2][kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x;
+    int head = __ldg(p.ring_state), count = __ldg(p.ring_state + 1);
+    const bool bad_ring = head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages;
+    if (bad_ring) head = count = 0;   // nothing can be handed out
+
+    if (b == p.B) {
+        // The ring's state after this step: the largest granted cum, and all returned pages.
+        if (blockIdx.y != 0) return;
+        const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+        const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
+        long long grow = 0, shrink = 0;
+        bool bad, any_bad = false;
+        for (int x = lo; x < hi; ++x) {
+            const Demand d = plan_demand(p, x, bad);
+            grow += d.grow, shrink += d.shrink;
+            any_bad |= bad;
+        }
+        // Exclusive prefix of this thread's requests, then its largest cum within the count.
+        long long scan = grow;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += up;
+        }
+        shrink = warp_sum(shrink);
+        if (lane == 31) part[0][warp] = scan;
+        if (lane == 0) part[1][warp] = shrink;
+        __syncthreads();
+        long long cum = scan - grow;
+        for (int x = 0; x < warp; ++x) cum += part[0][x];
+        int taken = 0;
+        for (int x = lo; x < hi; ++x) {
+            cum += plan_demand(p, x, bad).grow;
+            if (cum <= count) taken = static_cast<int>(cum);
+        }
+        long long returned = 0;
+        for (int x = 0; x < kPlanThreads / 32; ++x) returned += part[1][x];
+        __syncthreads();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+        if (lane == 0) part[0][warp] = taken;
+        any_bad = __syncthreads_or(any_bad);
+        if (tid == 0) {
+            for (int x = 0; x < kPlanThreads / 32; ++x) taken = max(taken, static_cast<int>(part[0][x]));
+            const long long left = count - taken + returned;
+            p.ring_state_out[0] = ring_index(p, static_cast<long long>(head) + taken);
+            p.ring_state_out[1] = static_cast<int>(min(left, static_cast<long long>(p.num_pages)));
+            if (any_bad || bad_ring || count + returned > p.num_pages) atomicOr(&g_status, kStatusBadLength);
+        }
+        return;
+    }
+
+    const int t0 = blockIdx.y * kPlanSlots;
+    bool bad;
+    long long before = 0, back = 0;
+    for (int x = tid; x < b; x += kPlanThreads) {
+        const Demand d = plan_demand(p, x, bad);
+        before += d.grow, back += d.shrink;
+    }
+    const Demand mine = plan_demand(p, b, bad);
+    const int ctx = __ldg(p.ctx_lens + b), held = __ldg(p.num_blocks + b);
+    before = warp_sum(before);
+    back = warp_sum(back);
+    if (lane == 0) part[0][warp] = before, part[1][warp] = back;
+    __syncthreads();
+    before = back = 0;
+#pragma unroll
+    for (int x = 0; x < kPlanThreads / 32; ++x) before += part[0][x], back += part[1][x];
+
+    const bool ok = mine.grow == 0 || before + mine.grow <= count;
+    const int granted = ok ? mine.granted : 0;
+    int* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
+    const long long take = head + before;   // ring position of this request's first new page
+    if (blockIdx.y == 0) {
+        if (tid == 0) {
+            p.granted[b] = granted;
+            p.num_blocks_out[b] = ok ? mine.need : held;
+        }
+        if (ok) {
+            for (int i = tid; i < mine.grow; i += kPlanThreads) row[held + i] = p.free_ring[ring_index(p, take + i)];
+            for (int i = tid; i < mine.shrink; i += kPlanThreads)
+                p.free_ring[ring_index(p, static_cast<long long>(head) + count + back + i)] = row[mine.need + i];
+        }
+    }
+    int* out = p.slots + static_cast<size_t>(b) * p.T;
+    const int t1 = min(p.T, t0 + kPlanSlots);
+    for (int t = t0 + tid; t < t1; t += kPlanThreads) {
+        int slot = -1;
+        if (t < granted) {
+            const unsigned pos = static_cast<unsigned>(ctx) + t, blk = pos / static_cast<unsigned>(p.page_size);
+            // A page of this call comes from the ring: another block may still be writing it
+            // into the table.
+            const int page = static_cast<int>(blk) < held
+                                 ? row[blk]
+                                 : p.free_ring[ring_index(p, take + (static_cast<int>(blk) - held))];
+            if (page >= 0 && page < p.num_pages)
+                slot = page * p.page_size + static_cast<int>(pos - blk * p.page_size);
+            else
+                atomicOr(&g_status, kStatusBadLength);
+        }
+        out[t] = slot;
+    }
+}
+
+// ------------------------------------------------------------------ tree_plan
+//
+// depth[t] = steps from node t to its root; mask[t] = {t} united with mask[parent[t]].
+// Pointer jumping: each round every node unites its set with that of its current
+// ancestor link, adds the link's depth and doubles the link, so a chain of T nodes
+// takes log2 T rounds.  One block per tree, one thread per node; bounded by the launch.
+
+constexpr int kTreeWords = kMaxTree / 32;
+
+__global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const TreePlanParams p) {
+    __shared__ uint32_t sets[kMaxTree][kTreeWords + 1];
+    __shared__ int links[kMaxTree], depths[kMaxTree];
+    const int b = blockIdx.x, t = threadIdx.x;
+    int n = __ldg(p.lens + b);
+    bool bad_len = n < 0 || n > p.T;
+    n = min(max(n, 0), p.T);
+    int link = -1;
+    bool bad = false;
+    if (t < n) {
+        link = __ldg(p.parents + static_cast<size_t>(b) * p.T + t);
+        bad = link < -1 || link >= t;   // a parent comes before its children
+        if (bad) link = -1;
+    }
+    int depth = link >= 0 ? 1 : 0;
+    uint32_t set[kTreeWords];
+#pragma unroll
+    for (int k = 0; k < kTreeWords; ++k) set[k] = (t < n && (t >> 5) == k) ? 1u << (t & 31) : 0u;
+    while (__syncthreads_or(link >= 0)) {
+#pragma unroll
+        for (int k = 0; k < kTreeWords; ++k) sets[t][k] = set[k];
+        links[t] = link;
+        depths[t] = depth;
+        __syncthreads();
+        if (link >= 0) {
+#pragma unroll
+            for (int k = 0; k < kTreeWords; ++k) set[k] |= sets[link][k];
+            depth += depths[link];
+            link = links[link];
+        }
+    }
+    if (t < p.T) {
+        const size_t at = static_cast<size_t>(b) * p.T + t;
+        const int words = (p.T + 31) / 32;
+        p.depth[at] = depth;
+#pragma unroll
+        for (int k = 0; k < kTreeWords; ++k)
+            if (k < words) p.mask[at * words + k] = static_cast<int>(set[k]);
+    }
+    if (bad) atomicOr(&g_status, kStatusBadTree);
+    if (bad_len && t == 0) atomicOr(&g_status, kStatusBadLength);
+}
+
+// ------------------------------------------------------------------ kv_append
+//
+// q'[c] = q[c] * wq[c] / sqrt(mean_c q[c]^2 + eps), the same for k with wk, both over one
+// head's d elements, the sum of squares in fp32; rows of k' and v go to cache row
+// slots[token].  One pass: every element is read once and written once, so the call is
+// bounded by HBM.  A head row is held by LANES threads, 16 bytes each (two vectors each
+// for 256 fp32 elements), and a thread has kAppendRows rows in flight.
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 4;
+
+template <typename T>
+struct Vec;   // 16 bytes of T as floats
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                          pack_bf16x2(f[6], f[7]));
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendParams p) {
+    constexpr int N = Vec<T>::N;
+    constexpr int kVecs = D / N;                       // 16-byte vectors of a head row
+    constexpr int LANES = kVecs < 32 ? kVecs : 32;     // threads of a head row
+    constexpr int VPL = kVecs / LANES;                 // vectors of a thread
+    constexpr int kRows = kAppendThreads / LANES;      // rows of a block and pass
+    const int sub = threadIdx.x % LANES;
+    const unsigned heads = static_cast<unsigned>(p.heads_q + 2 * p.Hkv);
+    const unsigned rows = static_cast<unsigned>(p.ntok) * heads;
+    const unsigned r0 = blockIdx.x * static_cast<unsigned>(kRows * kAppendRows) + threadIdx.x / LANES;
+
+    uint4 x[kAppendRows][VPL];
+    T* dst[kAppendRows];
+    const float* gain[kAppendRows];
+#pragma unroll
+    for (int u = 0; u < kAppendRows; ++u) {
+        const unsigned row = r0 + u * kRows;
+        dst[u] = nullptr;
+        gain[u] = nullptr;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) x[u][v] = make_uint4(0u, 0u, 0u, 0u);
+        if (row >= rows) continue;
+        const unsigned tok = row / heads;
+        int h = static_cast<int>(row - tok * heads);
+        const int slot = __ldg(p.slots + tok);
+        const T* src;
+        T* to;
+        if (h < p.heads_q) {
+            src = static_cast<const T*>(p.q) + static_cast<size_t>(tok) * p.q_stride + h * D;
+            to = static_cast<T*>(p.q_out) + (static_cast<size_t>(tok) * p.heads_q + h) * D;
+            gain[u] = p.q_weight;
+        } else {
+            h -= p.heads_q;
+            const bool is_v = h >= p.Hkv;
+            if (is_v) h -= p.Hkv;
+            src = static_cast<const T*>(is_v ? p.v : p.k) + static_cast<size_t>(tok) * (is_v ? p.v_stride : p.k_stride) +
+                  h * D;
+            to = static_cast<T*>(is_v ? p.v_pages : p.k_pages) + (static_cast<size_t>(max(slot, 0)) * p.Hkv + h) * D;
+            if (!is_v) gain[u] = p.k_weight;
+        }
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) x[u][v] = __ldg(reinterpret_cast<const uint4*>(src) + v * LANES + sub);
+        // Rows without a slot are padding; a slot outside the pool is refused and reported.
+        if (slot >= 0 && slot < p.num_slots) dst[u] = to;
+        if (slot >= p.num_slots) atomicOr(&g_status, kStatusBadLength);
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendRows; ++u) {
+        float f[VPL][N];
+        float ss = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            Vec<T>::unpack(x[u][v], f[v]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) ss = fmaf(f[v][e], f[v][e], ss);
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (dst[u] == nullptr) continue;
+        if (gain[u] != nullptr) {
+            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[v][e] *= inv * __ldg(gain[u] + (v * LANES + sub) * N + e);
+                x[u][v] = Vec<T>::pack(f[v]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) reinterpret_cast<uint4*>(dst[u])[v * LANES + sub] = x[u][v];
+    }
+}
+
+// ------------------------------------------------------------------ kv_compact
+//
+// Cache row ctx_b + i <- cache row ctx_b + path[b, i] for i < path_lens[b], in place, in
+// every layer.  A path is strictly increasing, so path[i] >= i: going up in i, a row is
+// read before any move writes it.  A thread owns 16 bytes of the rows and moves them in
+// that order, kCompactBatch rows in flight: the rows a batch writes (i .. i + 7) lie below
+// every row a later batch reads.  No thread reads what another writes.
+
+constexpr int kCompactBatch = 8;
+
+__global__ void __launch_bounds__(128) kv_compact_kernel(const KvCompactParams p) {
+    __shared__ long long from[kMaxTree], to[kMaxTree];
+    const int b = blockIdx.y;
+    const int ctx = __ldg(p.ctx_lens + b), n = __ldg(p.path_lens + b);
+    const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
+    bool bad = n < 0 || n > p.A || ctx < 0, bad_path = false;
+    if (!bad) {
+        const int* path = p.path + static_cast<size_t>(b) * p.A;
+        const int* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            const int x = __ldg(path + i);
+            if (x < i || (i > 0 && __ldg(path + i - 1) >= x)) {
+                bad_path = true;
+                continue;
+            }
+            const long long s = static_cast<long long>(ctx) + x, d = static_cast<long long>(ctx) + i;
+            if (s >= cap) {
+                bad = true;
+                continue;
+            }
+            const int ps = __ldg(table + s / p.page_size), pd = __ldg(table + d / p.page_size);
+            if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
+                bad = true;
+                continue;
+            }
+            from[i] = static_cast<long long>(ps) * p.page_size + s % p.page_size;
+            to[i] = static_cast<long long>(pd) * p.page_size + d % p.page_size;
+        }
+    }
+    const bool any_bad = __syncthreads_or(bad), any_path = __syncthreads_or(bad_path);
+    if (any_bad || any_path) {
+        if (threadIdx.x == 0) atomicOr(&g_status, (any_bad ? kStatusBadLength : 0u) | (any_path ? kStatusBadTree : 0u));
+        return;
+    }
+    const int col = blockIdx.x * blockDim.x + threadIdx.x;
+    if (col >= p.row_vecs) return;
+    const int layer = blockIdx.z >> 1;
+    uint4* base = static_cast<uint4*>((blockIdx.z & 1) ? p.v_pages : p.k_pages) +
+                  static_cast<size_t>(layer) * p.num_pages * p.page_size * p.row_vecs + col;
+    for (int i0 = 0; i0 < n; i0 += kCompactBatch) {
+        uint4 x[kCompactBatch];
+#pragma unroll
+        for (int u = 0; u < kCompactBatch; ++u)
+            if (i0 + u < n && from[i0 + u] != to[i0 + u]) x[u] = base[from[i0 + u] * p.row_vecs];
+#pragma unroll
+        for (int u = 0; u < kCompactBatch; ++u)
+            if (i0 + u < n && from[i0 + u] != to[i0 + u]) base[to[i0 + u] * p.row_vecs] = x[u];
+    }
+}
+
+template <typename T>
+cudaError_t launch_append(const KvAppendParams& p, int d, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(p.ntok) * (p.heads_q + 2 * p.Hkv);
+    const int vecs = d / Vec<T>::N;
+    const int per = kAppendThreads / (vecs < 32 ? vecs : 32) * kAppendRows;
+    const unsigned grid = static_cast<unsigned>((rows + per - 1) / per);
+    switch (d) {
+        case 32: kv_append_kernel<T, 32><<<grid, kAppendThreads, 0, stream>>>(p); break;
+        case 64: kv_append_kernel<T, 64><<<grid, kAppendThreads, 0, stream>>>(p); break;
+        case 128: kv_append_kernel<T, 128><<<grid, kAppendThreads, 0, stream>>>(p); break;
+        case 256: kv_append_kernel<T, 256><<<grid, kAppendThreads, 0, stream>>>(p); break;
+        default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
+    const dim3 grid(p.B + 1, std::max(1, (p.T + kPlanSlots - 1) / kPlanSlots));
+    page_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream) {
+    tree_plan_kernel<<<p.B, (p.T + 31) / 32 * 32, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, int d, cudaStream_t stream) {
+    return bf16 ? launch_append<__nv_bfloat16>(p, d, stream) : launch_append<float>(p, d, stream);
+}
+
+cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream) {
+    const int threads = std::min(128, (p.row_vecs + 31) / 32 * 32);
+    const dim3 grid((p.row_vecs + threads - 1) / threads, p.B, 2 * p.layers);
+    kv_compact_kernel<<<grid, threads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace relbias

@@ -13,6 +13,7 @@ __device__ unsigned int g_status = 0;
 
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBadLength = 2u;   // a device-side length or page index was out of range
+constexpr unsigned kStatusBadTree = 4u;     // a device-side tree (parents, depths or path) was malformed
 constexpr float kLn2 = 0.6931471805599453f;
 // A single wait longer than this is treated as a hang (nanoseconds).  Kernels read
 // the limit from g_wait_limit_ns, which the host may lower (relbias_set_wait_limit_ns)

@@ -19,6 +19,8 @@
 #include "prefill_sm100.cu"
 #include "backward_fp32.cu"
 #include "backward_sm100.cu"
+#include "paged_ops.cu"
+#include "tree_sm100.cu"
 
 namespace relbias {
 namespace {
@@ -774,7 +776,10 @@ extern "C" int relbias_set_wait_limit_ns(unsigned long long ns) {
     return e == cudaSuccess ? RELBIAS_OK : cuda_fail(e, "setting the wait limit");
 }
 
-extern "C" int relbias_version(void) { return 701; }
+extern "C" int relbias_version(void) { return 800; }
 
 // The allocation-free decode variant (its own file: it owns a static device array).
 #include "decode_noalloc.cu"
+
+// The serving-step operators over a paged cache.
+#include "paged_abi.cu"

@@ -23,6 +23,7 @@ RELBIAS_ERR_UNSUPPORTED = -2
 RELBIAS_ERR_CUDA = -3
 RELBIAS_STATUS_TIMEOUT = 1
 RELBIAS_STATUS_BAD_LENGTH = 2
+RELBIAS_STATUS_BAD_TREE = 4
 RELBIAS_BF16 = 0
 RELBIAS_FP32 = 1
 
@@ -31,6 +32,7 @@ _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "relbias_attn_fwd": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _VP]),
     "relbias_attn_fwd_chunk": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I,
@@ -54,6 +56,12 @@ SIGNATURES = {
     "relbias_attn_bwd": (_I, [_VP] * 13 + [_I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _VP, _SZ, _VP]),
     "relbias_attn_bwd_bank_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "relbias_attn_bwd_bank": (_I, [_VP] * 13 + [_I] * 9 + [_F, _I, _I, _VP, _SZ, _VP]),
+    "relbias_page_plan": (_I, [_VP] * 10 + [_I] * 5 + [_VP]),
+    "relbias_tree_plan": (_I, [_VP] * 4 + [_I] * 2 + [_VP]),
+    "relbias_kv_append": (_I, [_VP] * 9 + [_I] * 4 + [_LL] * 3 + [_I] * 2 + [_F, _I, _VP]),
+    "relbias_attn_tree_paged_workspace_size": (_SZ, [_I] * 7),
+    "relbias_attn_tree_paged": (_I, [_VP] * 12 + [_I] * 11 + [_F, _I, _I, _VP, _SZ, _VP]),
+    "relbias_kv_compact": (_I, [_VP] * 6 + [_I] * 9 + [_VP]),
     "relbias_last_error": (ctypes.c_char_p, []),
     "relbias_device_status": (_I, [_I]),
     "relbias_set_wait_limit_ns": (_I, [ctypes.c_ulonglong]),
@@ -465,6 +473,217 @@ def attn_bwd_bank(q, k, v, rs, proj, o, lse, dout, window: int, R: int, scale: f
                                      _dtype_code(q), _ptr(workspace), ws_bytes, _stream_handle(stream, q.device))
     _check(rc)
     return g
+
+# ---------------------------------------------------------------- a speculative-decoding step over a paged cache
+
+
+def _on_device(ref, **tensors):
+    """Checks that every tensor given is a dense CUDA tensor on `ref`'s device."""
+    dev = ref.device
+    for name, t in tensors.items():
+        if t is not None and not (t.is_cuda and t.device == dev and t.is_contiguous()):
+            raise ValueError("%s must be a contiguous CUDA tensor on %s" % (name, dev))
+
+
+def _i32(shape, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or t.shape != shape:
+            raise ValueError("%s must be int32 %s, got %s %s" % (name, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+def _call(fn, ref, stream, *args):
+    """fn(*args, stream) with ref's device current, on `stream` or that device's current stream."""
+    index = ref.device.index
+    if index == torch.cuda.current_device():
+        _check(fn(*args, (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream))
+
+
+def page_plan(ctx_lens, new_lens, num_blocks, block_table, free_ring, ring_state, page_size: int, T: int, slots=None,
+              granted=None, num_blocks_out=None, ring_state_out=None, stream=None):
+    """Block tables and slot maps of a step, built on the GPU from request lengths.
+    ctx_lens, new_lens, num_blocks [B] int32: rows in the cache, rows to add (at most T)
+    and pages held; block_table [B,max_pages] and free_ring [num_pages] int32, updated in
+    place; ring_state [2] int32 (head, count).  Request b then holds exactly the pages its
+    ctx_lens[b] + new_lens[b] rows need (surplus pages go back to the ring), or is refused
+    and keeps what it had if the ring runs out.  Returns (slots [B,T], granted [B],
+    num_blocks [B], ring_state [2]), new int32 tensors unless given; slots holds the cache
+    row of each new row, -1 past granted[b].  See relbias_page_plan in
+    include/relbias_attn.h."""
+    _need(ctx_lens.dim() == 1 and block_table.dim() == 2 and free_ring.dim() == 1,
+          "ctx_lens [B], block_table [B,max_pages], free_ring [num_pages]")
+    B, T = ctx_lens.shape[0], int(T)
+    _i32((B,), ctx_lens=ctx_lens, new_lens=new_lens, num_blocks=num_blocks)
+    _i32((B, block_table.shape[1]), block_table=block_table)
+    _i32(free_ring.shape, free_ring=free_ring)
+    _i32((2,), ring_state=ring_state)
+    slots = ctx_lens.new_empty((B, T)) if slots is None else slots
+    granted = torch.empty_like(ctx_lens) if granted is None else granted
+    num_blocks_out = torch.empty_like(ctx_lens) if num_blocks_out is None else num_blocks_out
+    ring_state_out = torch.empty_like(ring_state) if ring_state_out is None else ring_state_out
+    _i32((B, T), slots=slots)
+    _i32((B,), granted=granted, num_blocks_out=num_blocks_out)
+    _i32((2,), ring_state_out=ring_state_out)
+    _on_device(ctx_lens, ctx_lens=ctx_lens, new_lens=new_lens, num_blocks=num_blocks, block_table=block_table,
+               free_ring=free_ring, ring_state=ring_state, slots=slots, granted=granted,
+               num_blocks_out=num_blocks_out, ring_state_out=ring_state_out)
+    _call(lib().relbias_page_plan, ctx_lens, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), num_blocks.data_ptr(),
+          num_blocks_out.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(), ring_state.data_ptr(),
+          ring_state_out.data_ptr(), granted.data_ptr(), slots.data_ptr(), B, T, int(page_size),
+          block_table.shape[1], free_ring.shape[0])
+    return slots, granted, num_blocks_out, ring_state_out
+
+
+def tree_plan(parents, tree_lens, depth=None, mask=None, stream=None):
+    """Positions and ancestor masks of drafted trees.  parents [B,T] int32 (the parent of
+    each node, which comes before it; -1: a root), tree_lens [B] int32; T <= 128.  Returns
+    (depth [B,T], mask [B,T,ceil(T/32)]) int32: bit s of node t's words is set if s is t or
+    an ancestor of t."""
+    _need(parents.dim() == 2, "parents [B,T]")
+    B, T = parents.shape
+    words = (T + 31) // 32
+    _i32((B, T), parents=parents)
+    _i32((B,), tree_lens=tree_lens)
+    depth = torch.empty_like(parents) if depth is None else depth
+    mask = parents.new_empty((B, T, words)) if mask is None else mask
+    _i32((B, T), depth=depth)
+    _i32((B, T, words), mask=mask)
+    _on_device(parents, parents=parents, tree_lens=tree_lens, depth=depth, mask=mask)
+    _call(lib().relbias_tree_plan, parents, stream, parents.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(),
+          mask.data_ptr(), B, T)
+    return depth, mask
+
+
+def _token_stride(t, name: str, lead: tuple) -> int:
+    """Elements between the tokens of t [*lead, heads, d], whose heads are dense and whose
+    leading axes are evenly spaced (a slice of a projection's output, or dense)."""
+    d = t.shape[-1]
+    st = t.stride()
+    ok = t.shape[:-2] == lead and (d == 1 or st[-1] == 1) and (t.shape[-2] == 1 or st[-2] == d)
+    step = st[-3] if len(lead) and lead[-1] > 1 else None
+    for i in range(len(lead) - 2, -1, -1):
+        if lead[i] > 1:
+            if step is None:
+                step = st[i]
+            ok = ok and st[i] == step * math.prod(lead[i + 1:])
+    _need(ok, "%s must be [%s, heads, d] with dense heads and evenly spaced tokens" % (name, lead))
+    return t.shape[-2] * d if step is None else step
+
+
+def kv_append(k, v, slots, k_pages, v_pages, q=None, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None,
+              stream=None):
+    """New rows of a layer into its pages, with the per-head norm of queries and keys.
+    k, v [...,Hkv,d] and q [...,Hq,d] (bf16 or fp32; tokens may be strided, as slices of one
+    projection's output are), slots [...] int32 with the cache row of each token (< 0:
+    padding, skipped), k_pages/v_pages [num_pages,page_size,Hkv,d].  q_weight and k_weight
+    [d] fp32: x * weight / sqrt(mean(x^2) + eps) per head; None: no norm.  Returns q_out
+    [...,Hq,d] (None without q); its padding rows are left as they were."""
+    _need(k.dim() >= 3 and v.shape == k.shape and k_pages.dim() == 4 and v_pages.shape == k_pages.shape,
+          "k, v [...,Hkv,d], pages [num_pages,page_size,Hkv,d]")
+    lead = tuple(k.shape[:-2])
+    Hkv, d = k.shape[-2:]
+    _need(k_pages.shape[2] == Hkv and k_pages.shape[3] == d, "page heads or head dim do not match k")
+    _need(k.dtype == v.dtype == k_pages.dtype == v_pages.dtype and (q is None or q.dtype == k.dtype),
+          "q, k, v and the pages must share a dtype")
+    _i32(lead, slots=slots)
+    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(x is None or (x.shape == (d,) and x.dtype == torch.float32), "%s must be fp32 [d]" % name)
+    _need(q is not None or (q_weight is None and q_out is None), "q_weight and q_out need q")
+    Hq = 0
+    if q is not None:
+        _need(q.dim() == k.dim() and q.shape[-1] == d, "q [...,Hq,d] does not match k")
+        Hq = q.shape[-2]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must match q")
+    ntok = math.prod(lead)
+    strides = [0 if x is None else _token_stride(x, name, lead) for name, x in (("q", q), ("k", k), ("v", v))]
+    for x in (q, k, v):
+        _need(x is None or (x.is_cuda and x.device == k.device), "q, k and v must be CUDA tensors on one device")
+    _on_device(k, slots=slots, k_pages=k_pages, v_pages=v_pages, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+    code = _dtype_code(k)
+    _call(lib().relbias_kv_append, k, stream, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          slots.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), None if q is None else q_out.data_ptr(),
+          k_pages.data_ptr(), v_pages.data_ptr(), ntok, Hq, Hkv, d, *strides, k_pages.shape[0], k_pages.shape[1],
+          float(eps), code)
+    return q_out
+
+
+def tree_workspace_size(B: int, T: int, Hq: int, Hkv: int, max_ctx_len: int, d: int, window: int) -> int:
+    """Bytes of device scratch attn_tree_paged needs for this shape (on the current device)."""
+    return int(lib().relbias_attn_tree_paged_workspace_size(B, T, Hq, Hkv, int(max_ctx_len), d, int(window)))
+
+
+def attn_tree_paged(q, k_pages, v_pages, block_table, ctx_lens, tree_lens, depth, mask, r, w, window: int, R: int,
+                    max_ctx_len: int, scale: float | None = None, out=None, lse=None, workspace=None, stream=None,
+                    temp_n0: int = 0):
+    """Attention of drafted trees over a paged cache.  q [B,T,Hq,d] bf16 (sequence b's tree is
+    its first tree_lens[b] rows, whose keys and values are cache rows ctx_lens[b] + t),
+    k_pages/v_pages [num_pages,page_size,Hkv,d] bf16, block_table [B,max_pages], ctx_lens and
+    tree_lens [B], depth [B,T], mask [B,T,ceil(T/32)] int32 (as tree_plan returns them),
+    r [B,T,Hq] fp32, w [Hq,R] fp32; every ctx_lens[b] <= max_ctx_len.  Returns o [B,T,Hq,d]
+    (fills `lse` [B,Hq,T] fp32 when given); rows past tree_lens[b] are left as they were in
+    `out` (allocated, uninitialised, if None).  `workspace`: a byte tensor of at least
+    tree_workspace_size(...) bytes; allocated if None."""
+    _need(q.dim() == 4 and k_pages.dim() == 4 and v_pages.shape == k_pages.shape and block_table.dim() == 2,
+          "q [B,T,Hq,d], pages [num_pages,page_size,Hkv,d], block_table [B,max_pages]")
+    B, T, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = k_pages.shape
+    _need(dk == d, "page head dim %d != q head dim %d" % (dk, d))
+    _need(q.dtype == k_pages.dtype == v_pages.dtype, "q and pages must share a dtype")
+    max_pages = block_table.shape[1]
+    _i32((B, max_pages), block_table=block_table)
+    _i32((B,), ctx_lens=ctx_lens, tree_lens=tree_lens)
+    _i32((B, T), depth=depth)
+    _i32((B, T, (T + 31) // 32), mask=mask)
+    _need(r.shape == (B, T, Hq) and r.dtype == torch.float32, "r must be fp32 [B,T,Hq]")
+    _need(w is None or (w.shape == (Hq, R) and w.dtype == torch.float32), "w must be fp32 [Hq,R]")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    _need(lse is None or (lse.shape == (B, Hq, T) and lse.dtype == torch.float32), "lse must be fp32 [B,Hq,T]")
+    _on_device(q, q=q, k_pages=k_pages, v_pages=v_pages, block_table=block_table, ctx_lens=ctx_lens,
+               tree_lens=tree_lens, depth=depth, mask=mask, r=r, w=w, out=out, lse=lse, workspace=workspace)
+    code = _dtype_code(q)
+    if workspace is None:
+        with torch.cuda.device(q.device):
+            need = tree_workspace_size(B, T, Hq, Hkv, max_ctx_len, d, window)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _call(lib().relbias_attn_tree_paged, q, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          block_table.data_ptr(), ctx_lens.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(), mask.data_ptr(),
+          r.data_ptr(), None if w is None else w.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+          B, T, num_pages, page_size, max_pages, int(max_ctx_len), Hq, Hkv, d, int(window), int(R), float(scale),
+          int(temp_n0), code, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def kv_compact(k_pages, v_pages, block_table, ctx_lens, path, path_lens, stream=None):
+    """The accepted path's cache rows to the rows they keep, in place: row ctx_lens[b] + i
+    receives row ctx_lens[b] + path[b,i] for i < path_lens[b].  k_pages/v_pages
+    [num_pages,page_size,Hkv,d], or [layers,num_pages,page_size,Hkv,d] for all layers in one
+    call (bf16 or fp32); block_table [B,max_pages], ctx_lens [B], path [B,A] (strictly
+    increasing node indices), path_lens [B] int32; A <= 128."""
+    _need(k_pages.dim() in (4, 5) and v_pages.shape == k_pages.shape and v_pages.dtype == k_pages.dtype,
+          "pages [num_pages,page_size,Hkv,d] or [layers,num_pages,page_size,Hkv,d]")
+    _need(path.dim() == 2 and block_table.dim() == 2, "path [B,A], block_table [B,max_pages]")
+    B, A = path.shape
+    _i32((B, A), path=path)
+    _i32((B,), ctx_lens=ctx_lens, path_lens=path_lens)
+    _i32((B, block_table.shape[1]), block_table=block_table)
+    _on_device(k_pages, k_pages=k_pages, v_pages=v_pages, block_table=block_table, ctx_lens=ctx_lens, path=path,
+               path_lens=path_lens)
+    code = _dtype_code(k_pages)
+    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
+    num_pages, page_size, Hkv, d = k_pages.shape[-4:]
+    _call(lib().relbias_kv_compact, k_pages, stream, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+          ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), layers, B, A, num_pages, page_size,
+          block_table.shape[1], Hkv, d, code)
+
 
 def device_status(reset: bool = True) -> int:
     """Synchronise and return the kernels' status bits (RELBIAS_STATUS_*)."""

@@ -66,6 +66,7 @@ extern "C" {
 /* Bits of the device-side status word (relbias_device_status). */
 #define RELBIAS_STATUS_TIMEOUT   1u /* a bounded wait inside a kernel ran out             */
 #define RELBIAS_STATUS_BAD_LENGTH 2u /* a device-side sequence length or page index was out of range */
+#define RELBIAS_STATUS_BAD_TREE   4u /* a device-side parent, depth or accepted path was malformed */
 
 /* Element type of q, k, v and o.  r, w and lse are always fp32. */
 typedef enum {
@@ -367,6 +368,134 @@ RELBIAS_API int relbias_attn_bwd_bank(const void* q, const void* k, const void* 
                      int B, int T, int Hq, int Hkv, int d, int C, int proj_heads,
                      int window, int R, float scale, int temp_n0,
                      int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * One step of speculative decoding over a paged cache.  A serving loop that verifies a
+ * tree of drafted tokens calls, in this order: relbias_page_plan once per step (which
+ * pages, and which cache rows, the step's new tokens get), relbias_tree_plan once per
+ * step, then per layer relbias_kv_append and relbias_attn_tree_paged, and after the
+ * accepted path is known relbias_kv_compact.  The paged cache and its variable lengths
+ * are the ones of relbias_attn_decode_paged ("Thinking Machines dropped RoPE", closing
+ * section on kernel cost); the pages have no counterpart for drafting.
+ *
+ * relbias_page_plan: block tables and slot maps, on the GPU, from request lengths.
+ *   ctx_lens   [B]  int32  rows of request b already in the cache
+ *   new_lens   [B]  int32  rows it adds in this step, 0 <= new_lens[b] <= T
+ *   num_blocks [B]  int32  pages its block-table row holds; num_blocks_out [B] receives the
+ *                   number after the call (another array)
+ *   block_table [B, max_pages] int32, updated in place: request b holds exactly
+ *                   ceil((ctx_lens[b] + new_lens[b]) / page_size) pages afterwards; entries past
+ *                   that keep whatever they held.  A finished request (both lengths 0)
+ *                   returns all its pages, and one whose draft was cut short the surplus.
+ *   free_ring  [num_pages] int32, updated in place: a ring whose `count` entries from `head` on
+ *                   are the free pages; ring_state = {head, count}, and ring_state_out receives
+ *                   the state after the call (another array).  Pages are taken from the head
+ *                   in request order and returned at the tail in request order; a page
+ *                   returned by a call is handed out by a later one.
+ *   granted    [B]  int32  new_lens[b], or 0 for a refused request
+ *   slots      [B, T] int32  cache row (page * page_size + row in page) of new row t, -1 for
+ *                   t >= granted[b]
+ * A request is granted if it needs no further page, or if its pages and those of all
+ * earlier requests of the batch (refused ones included) are within `count`.  A refused
+ * request keeps its pages and its row.  A request with a length or page count out of
+ * range (or too long for max_pages) is refused and sets RELBIAS_STATUS_BAD_LENGTH, as does a
+ * ring state that cannot be.  All arrays are device memory; one launch.
+ * num_pages * page_size and max_pages * page_size < 2^31.
+ */
+RELBIAS_API int relbias_page_plan(const int* ctx_lens, const int* new_lens,
+                        const int* num_blocks, int* num_blocks_out,
+                        int* block_table, int* free_ring,
+                        const int* ring_state, int* ring_state_out,
+                        int* granted, int* slots,
+                        int B, int T, int page_size, int max_pages, int num_pages,
+                        void* stream);
+
+/*
+ * relbias_tree_plan: positions and ancestor masks of drafted trees.
+ *   parents   [B, T] int32  parent node of each node, -1 for a root (a node that follows the
+ *                    cache's last row directly); a parent comes before its children
+ *   tree_lens [B]    int32  nodes of each tree, at most T
+ *   depth     [B, T] int32  steps from the node to its root (output)
+ *   mask      [B, T, ceil(T / 32)] int32  bit s of node t's words: s is t or an ancestor of t
+ *                    (output); depth and mask of nodes past tree_lens[b] are 0
+ *   T <= 128.  A parent not below its child is taken as -1 and sets RELBIAS_STATUS_BAD_TREE; a
+ *   length out of range is clamped and sets RELBIAS_STATUS_BAD_LENGTH.
+ */
+RELBIAS_API int relbias_tree_plan(const int* parents, const int* tree_lens,
+                        int* depth, int* mask, int B, int T, void* stream);
+
+/*
+ * relbias_kv_append: new rows of a layer into its pages, with the per-head norm of queries
+ * and keys in the same pass ("Thinking Machines dropped RoPE", the logit-scaling
+ * paragraph: queries and keys are normalised per head; there is no rotation).
+ *   q [ntok, Hq, d], k and v [ntok, Hkv, d]: dtype; a token's heads are dense, tokens lie
+ *     q_stride, k_stride, v_stride elements apart (slices of one projection's output are
+ *     fine); q may be NULL (then q_out is too)
+ *   slots [ntok] int32: cache row of each token, < 0 for padding: a padding token's q_out row
+ *     is left as it was and nothing is written to the cache.  Two tokens of a call must
+ *     not share a row.  A row outside the pool is skipped like padding and sets
+ *     RELBIAS_STATUS_BAD_LENGTH.
+ *   q_weight, k_weight [d] fp32: x * weight / sqrt(mean(x^2) + eps) over a head's d elements,
+ *     in fp32, rounded once; NULL: the rows are copied as they are
+ *   q_out [ntok, Hq, d] dtype; k_pages, v_pages [num_pages, page_size, Hkv, d] dtype
+ *   d in {32, 64, 128, 256}; RELBIAS_BF16 or RELBIAS_FP32; strides multiples of 16 bytes.
+ *   Outputs must not overlap inputs.
+ */
+RELBIAS_API int relbias_kv_append(const void* q, const void* k, const void* v, const int* slots,
+                        const float* q_weight, const float* k_weight,
+                        void* q_out, void* k_pages, void* v_pages,
+                        int ntok, int Hq, int Hkv, int d,
+                        long long q_stride, long long k_stride, long long v_stride,
+                        int num_pages, int page_size, float eps, int dtype, void* stream);
+
+/*
+ * relbias_attn_tree_paged: attention of drafted trees over a paged, variable-length cache.
+ * Sequence b has ctx_lens[b] prefix rows and a tree of tree_lens[b] nodes, whose keys and
+ * values are cache rows ctx_lens[b] + t.  Node t sits at position ctx_lens[b] + depth[b][t].
+ * It sees prefix row j at distance ctx_lens[b] + depth[b][t] - j, and node s, if bit s of its
+ * mask is set, at distance depth[b][t] - depth[b][s], where 0 <= distance (< window); logits,
+ * bias, temperature and softmax are those of relbias_attn_fwd with i - j replaced by that
+ * distance and n by its position + 1.  A tree of one node is relbias_attn_decode_paged's step.
+ *   q, o   [B, T, Hq, d]  bf16     r [B, T, Hq], w [Hq, R], lse [B, Hq, T] fp32 (lse may be NULL)
+ *   k_pages, v_pages [num_pages, page_size, Hkv, d] bf16, block_table [B, max_pages] int32
+ *   ctx_lens, tree_lens [B], depth [B, T], mask [B, T, ceil(T / 32)]: int32, device; depth and
+ *     mask as relbias_tree_plan writes them, or any other mask
+ *   max_ctx_len bounds every ctx_lens[b] and plans the key splits.
+ * Rows t >= tree_lens[b] of o and lse are left as they were.  A node that sees nothing gets
+ * o = 0 and lse = -inf.  Cache rows that no node of a sequence sees by position (past its
+ * tree, or before the window of its first node) may hold anything; the values of rows
+ * inside that range must be finite, those of masked nodes included.
+ * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; workspace of at
+ * least relbias_attn_tree_paged_workspace_size(...) bytes, 16-byte aligned, whose contents on
+ * entry do not matter.  Lengths out of range are clamped and page indices outside the pool
+ * read zeros (RELBIAS_STATUS_BAD_LENGTH); a depth outside [0, T) is clamped
+ * (RELBIAS_STATUS_BAD_TREE).
+ */
+RELBIAS_API size_t relbias_attn_tree_paged_workspace_size(int B, int T, int Hq, int Hkv, int max_ctx_len, int d,
+                                                int window);
+RELBIAS_API int relbias_attn_tree_paged(const void* q, const void* k_pages, const void* v_pages,
+                        const int* block_table, const int* ctx_lens, const int* tree_lens,
+                        const int* depth, const int* mask,
+                        const float* r, const float* w,
+                        void* o, float* lse,
+                        int B, int T, int num_pages, int page_size, int max_pages, int max_ctx_len,
+                        int Hq, int Hkv, int d,
+                        int window, int R, float scale, int temp_n0,
+                        int dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * relbias_kv_compact: the accepted path's rows to the rows they keep, in place: cache row
+ * ctx_lens[b] + i receives row ctx_lens[b] + path[b][i] for i < path_lens[b], in every layer.
+ *   k_pages, v_pages [layers, num_pages, page_size, Hkv, d] dtype (rows of a multiple of 16 bytes)
+ *   block_table [B, max_pages], ctx_lens [B], path [B, A], path_lens [B]: int32, device
+ *   A <= 128.  A path must be strictly increasing and start at 0 or more (a node's ancestors
+ *   come before it); a path that is not, or a row outside the table or the pool, leaves
+ *   that sequence's rows as they were and sets RELBIAS_STATUS_BAD_TREE or _BAD_LENGTH.
+ */
+RELBIAS_API int relbias_kv_compact(void* k_pages, void* v_pages, const int* block_table,
+                        const int* ctx_lens, const int* path, const int* path_lens,
+                        int layers, int B, int A, int num_pages, int page_size, int max_pages,
+                        int Hkv, int d, int dtype, void* stream);
 
 /* Description of the last failed call on this thread ("" if none).  The string
  * stays valid until the next library call on the same thread. */
