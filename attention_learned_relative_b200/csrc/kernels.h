@@ -195,8 +195,6 @@ cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream);
 
 // Attention of drafted trees over a paged cache (tree_sm100.cu).
 struct TreeAttnParams {
-    const __nv_bfloat16* q;          // [B, T, Hq, d]
-    const __nv_bfloat16 *k_pages, *v_pages;
     const int* block_table;          // [B, max_pages]
     const int* ctx_lens;             // [B] rows of the prefix
     const int* tree_lens;            // [B] nodes of the tree
@@ -206,13 +204,23 @@ struct TreeAttnParams {
     const float* w;                  // [Hq, R]
     __nv_bfloat16* o;                // [B, T, Hq, d]
     float* lse;                      // [B, Hq, T] or nullptr
+    float* part;                     // [B, T, Hq, nsplit, d + 4] partial records (nsplit > 1)
     int B, T, Hq, Hkv, G, words;
+    int groups;                      // pairs of row tiles of a full tree
+    int nsplit, tiles_per_split;     // runs of key tiles of the longest sequence
     int num_pages, page_size, max_pages, max_ctx;
+    int box_rows;                    // rows of a K/V box: the largest power of two up to 128 that divides a page
     int window, R;
     float scale_log2, inv_scale;
     int temp_n0;
     float inv_log_n0;
 };
-cudaError_t launch_tree_attn(const TreeAttnParams& p, int d, cudaStream_t stream);
+int tree_max_tiles(int T, int max_ctx, int window, int box_rows);
+int tree_num_splits(int items, int tiles, int sms);
+size_t tree_workspace_bytes(int B, int T, int Hq, int d, int nsplit);
+// tq: 128 / G tokens by G heads per box (make_map's `heads`); tk, tv over the page pool,
+// box_rows rows per box.
+cudaError_t launch_tree_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const TreeAttnParams& p, int d, cudaStream_t stream);
 
 }  // namespace relbias

@@ -178,11 +178,45 @@ extern "C" int relbias_kv_compact(void* k_pages, void* v_pages, const int* block
     return e == cudaSuccess ? RELBIAS_OK : cuda_fail(e, "cache compaction launch");
 }
 
+namespace relbias {
+namespace {
+// The launch plan of a tree attention call.  Splits are planned for any page size (16-row
+// boxes), so that the workspace does not depend on it.
+struct TreePlan {
+    int groups, nsplit, tiles_per_split;
+};
+TreePlan tree_launch_plan(int B, int T, int Hq, int Hkv, int max_ctx_len, int window, int sms) {
+    const int npt = 128 / (Hq / Hkv);
+    TreePlan x{};
+    x.groups = ((T + npt - 1) / npt + 1) / 2;
+    const int tiles = tree_max_tiles(T, max_ctx_len, window > 0 ? window : 0, 128);
+    const int ns = tree_num_splits(B * Hkv * x.groups, tiles, sms);
+    x.tiles_per_split = (tiles + ns - 1) / ns;
+    x.nsplit = (tiles + x.tiles_per_split - 1) / x.tiles_per_split;
+    return x;
+}
+int check_tree_shape(int B, int T, int Hq, int Hkv, int max_ctx_len, int d) {
+    if (T > kMaxTree) return fail(RELBIAS_ERR_UNSUPPORTED, "trees have at most %d nodes, got T = %d", kMaxTree, T);
+    if (max_ctx_len < 0) return fail(RELBIAS_ERR_ARG, "max_ctx_len (%d) must be >= 0", max_ctx_len);
+    if (max_ctx_len > 1 << 30) return fail(RELBIAS_ERR_UNSUPPORTED, "max_ctx_len (%d) is past 2^30", max_ctx_len);
+    if (d != 64 && d != 128)
+        return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention supports d in {64, 128}, got %d", d);
+    if (Hq / Hkv > 16)
+        return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention supports up to 16 query heads per key/value head");
+    if (B > 65535) return fail(RELBIAS_ERR_UNSUPPORTED, "at most 65535 sequences, got %d", B);
+    if (Hkv > 4096) return fail(RELBIAS_ERR_UNSUPPORTED, "at most 4096 key/value heads, got %d", Hkv);
+    return RELBIAS_OK;
+}
+}  // namespace
+}  // namespace relbias
+
 extern "C" size_t relbias_attn_tree_paged_workspace_size(int B, int T, int Hq, int Hkv, int max_ctx_len, int d,
                                                          int window) {
-    (void)window;
-    if (B < 1 || T < 1 || T > kMaxTree || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_ctx_len < 0 || d < 1) return 0;
-    return 16;
+    if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+    if (check_tree_shape(B, T, Hq, Hkv, max_ctx_len, d) != RELBIAS_OK) return 0;
+    DeviceInfo dev;
+    if (device_info(dev) != RELBIAS_OK) return 0;
+    return tree_workspace_bytes(B, T, Hq, d, tree_launch_plan(B, T, Hq, Hkv, max_ctx_len, window, dev.sms).nsplit);
 }
 
 extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
@@ -195,17 +229,12 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     int rc = check_common(B, T, Hq, Hkv, d, R, scale, w);
     if (rc != RELBIAS_OK) return rc;
     if (dtype != RELBIAS_BF16 && dtype != RELBIAS_FP32) return fail(RELBIAS_ERR_ARG, "unknown dtype %d", dtype);
-    if (T > kMaxTree) return fail(RELBIAS_ERR_UNSUPPORTED, "trees have at most %d nodes, got T = %d", kMaxTree, T);
     if ((rc = check_pool(num_pages, page_size, max_pages)) != RELBIAS_OK) return rc;
     if (page_size % 16 != 0) return fail(RELBIAS_ERR_ARG, "page_size (%d) must be a multiple of 16", page_size);
     if (max_ctx_len < 0 || static_cast<long long>(max_ctx_len) > static_cast<long long>(max_pages) * page_size)
         return fail(RELBIAS_ERR_ARG, "max_ctx_len (%d) must be in [0, max_pages * page_size]", max_ctx_len);
     if (dtype != RELBIAS_BF16) return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention is bf16 only");
-    if (d != 64 && d != 128)
-        return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention supports d in {64, 128}, got %d", d);
-    if (Hq / Hkv > 16)
-        return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention supports up to 16 query heads per key/value head");
-    if (B > 65535) return fail(RELBIAS_ERR_UNSUPPORTED, "at most 65535 sequences, got %d", B);
+    if ((rc = check_tree_shape(B, T, Hq, Hkv, max_ctx_len, d)) != RELBIAS_OK) return rc;
     if (B == 0 || T == 0) return RELBIAS_OK;
     if (any_null(q, k_pages, v_pages, static_cast<const void*>(o), static_cast<const void*>(workspace)) ||
         any_null(block_table, ctx_lens, tree_lens, depth, mask) || r == nullptr)
@@ -221,9 +250,6 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
         return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention needs compute capability 10.0 (sm_100a), found %d.%d",
                     dev.major, dev.minor);
     TreeAttnParams p{};
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
-    p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
     p.block_table = block_table;
     p.ctx_lens = ctx_lens;
     p.tree_lens = tree_lens;
@@ -249,9 +275,19 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.inv_scale = 1.0f / scale;
     p.temp_n0 = temp_n0 > 1 ? temp_n0 : 0;
     p.inv_log_n0 = temp_n0 > 1 ? static_cast<float>(1.0 / std::log(static_cast<double>(temp_n0))) : 0.0f;
-    const size_t need = relbias_attn_tree_paged_workspace_size(B, T, Hq, Hkv, max_ctx_len, d, window);
+    const TreePlan plan = tree_launch_plan(B, T, Hq, Hkv, max_ctx_len, window, dev.sms);
+    p.groups = plan.groups;
+    p.nsplit = plan.nsplit;
+    p.tiles_per_split = plan.tiles_per_split;
+    p.part = static_cast<float*>(workspace);
+    p.box_rows = std::min(128, page_size & -page_size);
+    const size_t need = tree_workspace_bytes(B, T, Hq, d, p.nsplit);
     if (ws_bytes < need)
         return fail(RELBIAS_ERR_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
-    const cudaError_t e = launch_tree_attn(p, d, static_cast<cudaStream_t>(stream));
+    CUtensorMap tq, tk, tv;
+    if ((rc = make_map(&tq, q, B, T, Hq, d, 128 / p.G, 0, p.G)) != RELBIAS_OK) return rc;
+    if ((rc = make_map(&tk, k_pages, num_pages, page_size, Hkv, d, p.box_rows)) != RELBIAS_OK) return rc;
+    if ((rc = make_map(&tv, v_pages, num_pages, page_size, Hkv, d, p.box_rows)) != RELBIAS_OK) return rc;
+    const cudaError_t e = launch_tree_attn(tq, tk, tv, p, d, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RELBIAS_OK : cuda_fail(e, "tree attention launch");
 }

@@ -81,10 +81,11 @@ int device_info(DeviceInfo& info) {
 }
 
 // 4-D bf16 tensor map over a [B, T, H, d] tensor, box = 64 head-dim columns x
-// `rows` tokens of one head, 128-byte swizzle, zero fill outside the tensor.  With
+// `rows` tokens of `heads` heads, 128-byte swizzle, zero fill outside the tensor.  With
 // T_alloc > T the tensor is the first T rows of a [B, T_alloc, H, d] allocation: rows
 // past T read as zeros.
-int make_map(CUtensorMap* m, const void* ptr, int B, int T, int H, int d, int rows, int T_alloc = 0) {
+int make_map(CUtensorMap* m, const void* ptr, int B, int T, int H, int d, int rows, int T_alloc = 0,
+             int heads = 1) {
     std::string why;
     EncodeTiledFn fn = encode_fn(why);
     if (fn == nullptr) return fail(RELBIAS_ERR_CUDA, "%s", why.c_str());
@@ -93,7 +94,7 @@ int make_map(CUtensorMap* m, const void* ptr, int B, int T, int H, int d, int ro
     const int Ta = T_alloc > T ? T_alloc : T;
     cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(H) * d * 2,
                              static_cast<cuuint64_t>(Ta) * H * d * 2};
-    cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(rows), 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
