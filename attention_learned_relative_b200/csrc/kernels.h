@@ -204,10 +204,14 @@ struct TreeAttnParams {
     const float* w;                  // [Hq, R]
     __nv_bfloat16* o;                // [B, T, Hq, d]
     float* lse;                      // [B, Hq, T] or nullptr
-    float* part;                     // [B, T, Hq, nsplit, d + 4] partial records (nsplit > 1)
+    int4* cuts;                      // [runs * groups] workspace: the cut segment that starts in each run
+    float* part;                     // [runs * groups, 2, part_rows, d + 4] workspace: partials of cut segments
     int B, T, Hq, Hkv, G, words;
     int groups;                      // pairs of row tiles of a full tree
-    int nsplit, tiles_per_split;     // runs of key tiles of the longest sequence
+    int runs;                        // runs of a pair's tile stream
+    int part_rows;                   // rows of a partial
+    int tab_bufs;                    // buffers of bias slices
+    bool cuttable;                   // some segment may have more than one key tile
     int num_pages, page_size, max_pages, max_ctx;
     int box_rows;                    // rows of a K/V box: the largest power of two up to 128 that divides a page
     int window, R;
@@ -215,9 +219,14 @@ struct TreeAttnParams {
     int temp_n0;
     float inv_log_n0;
 };
+// Launch plan of a tree attention call, from what the host knows, and its workspace:
+// cut_bytes of `cuts`, then the partials.
+struct TreeLaunch {
+    int groups, runs, part_rows;
+    size_t cut_bytes, bytes;
+};
 int tree_max_tiles(int T, int max_ctx, int window, int box_rows);
-int tree_num_splits(int items, int tiles, int sms);
-size_t tree_workspace_bytes(int B, int T, int Hq, int d, int nsplit);
+TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int window, int d, int sms);
 // tq: 128 / G tokens by G heads per box (make_map's `heads`); tk, tv over the page pool,
 // box_rows rows per box.
 cudaError_t launch_tree_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

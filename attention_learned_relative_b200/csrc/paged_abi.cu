@@ -180,21 +180,6 @@ extern "C" int relbias_kv_compact(void* k_pages, void* v_pages, const int* block
 
 namespace relbias {
 namespace {
-// The launch plan of a tree attention call.  Splits are planned for any page size (16-row
-// boxes), so that the workspace does not depend on it.
-struct TreePlan {
-    int groups, nsplit, tiles_per_split;
-};
-TreePlan tree_launch_plan(int B, int T, int Hq, int Hkv, int max_ctx_len, int window, int sms) {
-    const int npt = 128 / (Hq / Hkv);
-    TreePlan x{};
-    x.groups = ((T + npt - 1) / npt + 1) / 2;
-    const int tiles = tree_max_tiles(T, max_ctx_len, window > 0 ? window : 0, 128);
-    const int ns = tree_num_splits(B * Hkv * x.groups, tiles, sms);
-    x.tiles_per_split = (tiles + ns - 1) / ns;
-    x.nsplit = (tiles + x.tiles_per_split - 1) / x.tiles_per_split;
-    return x;
-}
 int check_tree_shape(int B, int T, int Hq, int Hkv, int max_ctx_len, int d) {
     if (T > kMaxTree) return fail(RELBIAS_ERR_UNSUPPORTED, "trees have at most %d nodes, got T = %d", kMaxTree, T);
     if (max_ctx_len < 0) return fail(RELBIAS_ERR_ARG, "max_ctx_len (%d) must be >= 0", max_ctx_len);
@@ -216,7 +201,7 @@ extern "C" size_t relbias_attn_tree_paged_workspace_size(int B, int T, int Hq, i
     if (check_tree_shape(B, T, Hq, Hkv, max_ctx_len, d) != RELBIAS_OK) return 0;
     DeviceInfo dev;
     if (device_info(dev) != RELBIAS_OK) return 0;
-    return tree_workspace_bytes(B, T, Hq, d, tree_launch_plan(B, T, Hq, Hkv, max_ctx_len, window, dev.sms).nsplit);
+    return tree_launch_plan(B, T, Hkv, Hq / Hkv, max_ctx_len, std::max(window, 0), d, dev.sms).bytes;
 }
 
 extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
@@ -275,15 +260,17 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.inv_scale = 1.0f / scale;
     p.temp_n0 = temp_n0 > 1 ? temp_n0 : 0;
     p.inv_log_n0 = temp_n0 > 1 ? static_cast<float>(1.0 / std::log(static_cast<double>(temp_n0))) : 0.0f;
-    const TreePlan plan = tree_launch_plan(B, T, Hq, Hkv, max_ctx_len, window, dev.sms);
-    p.groups = plan.groups;
-    p.nsplit = plan.nsplit;
-    p.tiles_per_split = plan.tiles_per_split;
-    p.part = static_cast<float*>(workspace);
     p.box_rows = std::min(128, page_size & -page_size);
-    const size_t need = tree_workspace_bytes(B, T, Hq, d, p.nsplit);
-    if (ws_bytes < need)
-        return fail(RELBIAS_ERR_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
+    const TreeLaunch plan = tree_launch_plan(B, T, Hkv, p.G, max_ctx_len, p.window, d, dev.sms);
+    if (ws_bytes < plan.bytes)
+        return fail(RELBIAS_ERR_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes,
+                    plan.bytes);
+    p.groups = plan.groups;
+    p.runs = plan.runs;
+    p.part_rows = plan.part_rows;
+    p.cuttable = tree_max_tiles(T, max_ctx_len, p.window, p.box_rows) > 1;
+    p.cuts = static_cast<int4*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cut_bytes);
     CUtensorMap tq, tk, tv;
     if ((rc = make_map(&tq, q, B, T, Hq, d, 128 / p.G, 0, p.G)) != RELBIAS_OK) return rc;
     if ((rc = make_map(&tk, k_pages, num_pages, page_size, Hkv, d, p.box_rows)) != RELBIAS_OK) return rc;

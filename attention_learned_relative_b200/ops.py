@@ -477,28 +477,37 @@ def attn_bwd_bank(q, k, v, rs, proj, o, lse, dout, window: int, R: int, scale: f
 # ---------------------------------------------------------------- a speculative-decoding step over a paged cache
 
 
-def _on_device(ref, **tensors):
-    """Checks that every tensor given is a dense CUDA tensor on `ref`'s device."""
-    dev = ref.device
-    for name, t in tensors.items():
-        if t is not None and not (t.is_cuda and t.device == dev and t.is_contiguous()):
-            raise ValueError("%s must be a contiguous CUDA tensor on %s" % (name, dev))
+# These calls take a few microseconds on the device, so their checks are kept short: one
+# comparison per tensor, no copies, and only tensors that the caller gave are looked at.
 
 
-def _i32(shape, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.shape != shape:
-            raise ValueError("%s must be int32 %s, got %s %s" % (name, tuple(shape), t.dtype, tuple(t.shape)))
+def _dense(t, name: str, dev: int, dtype, shape):
+    """Checks that `t` is a dense CUDA tensor of this device, dtype and shape."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor %s on cuda:%d, got %s %s on %s" % (
+            name, str(dtype).replace("torch.", ""), tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
 
 
-def _call(fn, ref, stream, *args):
-    """fn(*args, stream) with ref's device current, on `stream` or that device's current stream."""
-    index = ref.device.index
-    if index == torch.cuda.current_device():
-        _check(fn(*args, (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream))
-    else:
-        with torch.cuda.device(index):
-            _check(fn(*args, (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream))
+def _device_of(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return dev
+
+
+def _on(dev: int, fn, *args):
+    """fn(*args) with device `dev` current."""
+    if dev == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _call(fn, dev: int, stream, *args):
+    """fn(*args, stream) with device `dev` current, on `stream` or that device's current stream."""
+    rc = _on(dev, fn, *args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if rc != RELBIAS_OK:
+        _check(rc)
 
 
 def page_plan(ctx_lens, new_lens, num_blocks, block_table, free_ring, ring_state, page_size: int, T: int, slots=None,
@@ -514,25 +523,35 @@ def page_plan(ctx_lens, new_lens, num_blocks, block_table, free_ring, ring_state
     include/relbias_attn.h."""
     _need(ctx_lens.dim() == 1 and block_table.dim() == 2 and free_ring.dim() == 1,
           "ctx_lens [B], block_table [B,max_pages], free_ring [num_pages]")
-    B, T = ctx_lens.shape[0], int(T)
-    _i32((B,), ctx_lens=ctx_lens, new_lens=new_lens, num_blocks=num_blocks)
-    _i32((B, block_table.shape[1]), block_table=block_table)
-    _i32(free_ring.shape, free_ring=free_ring)
-    _i32((2,), ring_state=ring_state)
-    slots = ctx_lens.new_empty((B, T)) if slots is None else slots
-    granted = torch.empty_like(ctx_lens) if granted is None else granted
-    num_blocks_out = torch.empty_like(ctx_lens) if num_blocks_out is None else num_blocks_out
-    ring_state_out = torch.empty_like(ring_state) if ring_state_out is None else ring_state_out
-    _i32((B, T), slots=slots)
-    _i32((B,), granted=granted, num_blocks_out=num_blocks_out)
-    _i32((2,), ring_state_out=ring_state_out)
-    _on_device(ctx_lens, ctx_lens=ctx_lens, new_lens=new_lens, num_blocks=num_blocks, block_table=block_table,
-               free_ring=free_ring, ring_state=ring_state, slots=slots, granted=granted,
-               num_blocks_out=num_blocks_out, ring_state_out=ring_state_out)
-    _call(lib().relbias_page_plan, ctx_lens, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), num_blocks.data_ptr(),
+    i32 = torch.int32
+    shape, T = ctx_lens.shape, int(T)
+    B, max_pages, num_pages = shape[0], block_table.shape[1], free_ring.shape[0]
+    dev = _device_of(ctx_lens, "ctx_lens")
+    _dense(ctx_lens, "ctx_lens", dev, i32, shape)
+    _dense(new_lens, "new_lens", dev, i32, shape)
+    _dense(num_blocks, "num_blocks", dev, i32, shape)
+    _dense(block_table, "block_table", dev, i32, (B, max_pages))
+    _dense(free_ring, "free_ring", dev, i32, (num_pages,))
+    _dense(ring_state, "ring_state", dev, i32, (2,))
+    if slots is None:
+        slots = ctx_lens.new_empty((B, T))
+    else:
+        _dense(slots, "slots", dev, i32, (B, T))
+    if granted is None:
+        granted = torch.empty_like(ctx_lens)
+    else:
+        _dense(granted, "granted", dev, i32, shape)
+    if num_blocks_out is None:
+        num_blocks_out = torch.empty_like(ctx_lens)
+    else:
+        _dense(num_blocks_out, "num_blocks_out", dev, i32, shape)
+    if ring_state_out is None:
+        ring_state_out = torch.empty_like(ring_state)
+    else:
+        _dense(ring_state_out, "ring_state_out", dev, i32, (2,))
+    _call(lib().relbias_page_plan, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), num_blocks.data_ptr(),
           num_blocks_out.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(), ring_state.data_ptr(),
-          ring_state_out.data_ptr(), granted.data_ptr(), slots.data_ptr(), B, T, int(page_size),
-          block_table.shape[1], free_ring.shape[0])
+          ring_state_out.data_ptr(), granted.data_ptr(), slots.data_ptr(), B, T, int(page_size), max_pages, num_pages)
     return slots, granted, num_blocks_out, ring_state_out
 
 
@@ -543,15 +562,19 @@ def tree_plan(parents, tree_lens, depth=None, mask=None, stream=None):
     an ancestor of t."""
     _need(parents.dim() == 2, "parents [B,T]")
     B, T = parents.shape
-    words = (T + 31) // 32
-    _i32((B, T), parents=parents)
-    _i32((B,), tree_lens=tree_lens)
-    depth = torch.empty_like(parents) if depth is None else depth
-    mask = parents.new_empty((B, T, words)) if mask is None else mask
-    _i32((B, T), depth=depth)
-    _i32((B, T, words), mask=mask)
-    _on_device(parents, parents=parents, tree_lens=tree_lens, depth=depth, mask=mask)
-    _call(lib().relbias_tree_plan, parents, stream, parents.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(),
+    words, i32 = (T + 31) // 32, torch.int32
+    dev = _device_of(parents, "parents")
+    _dense(parents, "parents", dev, i32, (B, T))
+    _dense(tree_lens, "tree_lens", dev, i32, (B,))
+    if depth is None:
+        depth = torch.empty_like(parents)
+    else:
+        _dense(depth, "depth", dev, i32, (B, T))
+    if mask is None:
+        mask = parents.new_empty((B, T, words))
+    else:
+        _dense(mask, "mask", dev, i32, (B, T, words))
+    _call(lib().relbias_tree_plan, dev, stream, parents.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(),
           mask.data_ptr(), B, T)
     return depth, mask
 
@@ -559,17 +582,20 @@ def tree_plan(parents, tree_lens, depth=None, mask=None, stream=None):
 def _token_stride(t, name: str, lead: tuple) -> int:
     """Elements between the tokens of t [*lead, heads, d], whose heads are dense and whose
     leading axes are evenly spaced (a slice of a projection's output, or dense)."""
-    d = t.shape[-1]
-    st = t.stride()
-    ok = t.shape[:-2] == lead and (d == 1 or st[-1] == 1) and (t.shape[-2] == 1 or st[-2] == d)
-    step = st[-3] if len(lead) and lead[-1] > 1 else None
-    for i in range(len(lead) - 2, -1, -1):
+    shape, st = t.shape, t.stride()
+    heads, d = shape[-2], shape[-1]
+    ok = shape[:-2] == lead and (d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d)
+    step, span = None, 1
+    for i in range(len(lead) - 1, -1, -1):   # axes of one token have no say
         if lead[i] > 1:
             if step is None:
                 step = st[i]
-            ok = ok and st[i] == step * math.prod(lead[i + 1:])
-    _need(ok, "%s must be [%s, heads, d] with dense heads and evenly spaced tokens" % (name, lead))
-    return t.shape[-2] * d if step is None else step
+            elif st[i] != step * span:
+                ok = False
+        span *= lead[i]
+    if not ok:
+        raise ValueError("%s must be [%s, heads, d] with dense heads and evenly spaced tokens" % (name, lead))
+    return heads * d if step is None else step
 
 
 def kv_append(k, v, slots, k_pages, v_pages, q=None, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None,
@@ -580,40 +606,43 @@ def kv_append(k, v, slots, k_pages, v_pages, q=None, q_weight=None, k_weight=Non
     padding, skipped), k_pages/v_pages [num_pages,page_size,Hkv,d].  q_weight and k_weight
     [d] fp32: x * weight / sqrt(mean(x^2) + eps) per head; None: no norm.  Returns q_out
     [...,Hq,d] (None without q); its padding rows are left as they were."""
-    _need(k.dim() >= 3 and v.shape == k.shape and k_pages.dim() == 4 and v_pages.shape == k_pages.shape,
-          "k, v [...,Hkv,d], pages [num_pages,page_size,Hkv,d]")
-    lead = tuple(k.shape[:-2])
-    Hkv, d = k.shape[-2:]
-    _need(k_pages.shape[2] == Hkv and k_pages.shape[3] == d, "page heads or head dim do not match k")
-    _need(k.dtype == v.dtype == k_pages.dtype == v_pages.dtype and (q is None or q.dtype == k.dtype),
-          "q, k, v and the pages must share a dtype")
-    _i32(lead, slots=slots)
-    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _need(x is None or (x.shape == (d,) and x.dtype == torch.float32), "%s must be fp32 [d]" % name)
-    _need(q is not None or (q_weight is None and q_out is None), "q_weight and q_out need q")
-    Hq = 0
-    if q is not None:
-        _need(q.dim() == k.dim() and q.shape[-1] == d, "q [...,Hq,d] does not match k")
+    _need(k.dim() >= 3 and k_pages.dim() == 4, "k, v [...,Hkv,d], pages [num_pages,page_size,Hkv,d]")
+    shape, dtype = k.shape, k.dtype
+    lead, Hkv, d = shape[:-2], shape[-2], shape[-1]
+    num_pages, page_size = k_pages.shape[:2]
+    dev = _device_of(k, "k")
+    _need(v.shape == shape and v.dtype is dtype and v.get_device() == dev, "v must match k")
+    _dense(k_pages, "k_pages", dev, dtype, (num_pages, page_size, Hkv, d))
+    _dense(v_pages, "v_pages", dev, dtype, (num_pages, page_size, Hkv, d))
+    _dense(slots, "slots", dev, torch.int32, lead)
+    if k_weight is not None:
+        _dense(k_weight, "k_weight", dev, torch.float32, (d,))
+    Hq = q_stride = 0
+    q_ptr = out_ptr = qw_ptr = None
+    if q is None:
+        _need(q_weight is None and q_out is None, "q_weight and q_out need q")
+    else:
+        _need(q.dim() == k.dim() and q.shape[-1] == d and q.dtype is dtype and q.get_device() == dev,
+              "q [...,Hq,d] does not match k")
         Hq = q.shape[-2]
+        q_stride = _token_stride(q, "q", lead)
+        if q_weight is not None:
+            _dense(q_weight, "q_weight", dev, torch.float32, (d,))
+            qw_ptr = q_weight.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _need(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must match q")
-    ntok = math.prod(lead)
-    strides = [0 if x is None else _token_stride(x, name, lead) for name, x in (("q", q), ("k", k), ("v", v))]
-    for x in (q, k, v):
-        _need(x is None or (x.is_cuda and x.device == k.device), "q, k and v must be CUDA tensors on one device")
-    _on_device(k, slots=slots, k_pages=k_pages, v_pages=v_pages, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
-    code = _dtype_code(k)
-    _call(lib().relbias_kv_append, k, stream, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          slots.data_ptr(), None if q_weight is None else q_weight.data_ptr(),
-          None if k_weight is None else k_weight.data_ptr(), None if q is None else q_out.data_ptr(),
-          k_pages.data_ptr(), v_pages.data_ptr(), ntok, Hq, Hkv, d, *strides, k_pages.shape[0], k_pages.shape[1],
-          float(eps), code)
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        else:
+            _dense(q_out, "q_out", dev, dtype, q.shape)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    _call(lib().relbias_kv_append, dev, stream, q_ptr, k.data_ptr(), v.data_ptr(), slots.data_ptr(), qw_ptr,
+          None if k_weight is None else k_weight.data_ptr(), out_ptr, k_pages.data_ptr(), v_pages.data_ptr(),
+          lead.numel(), Hq, Hkv, d, q_stride, _token_stride(k, "k", lead), _token_stride(v, "v", lead), num_pages,
+          page_size, float(eps), _dtype_code(k))
     return q_out
 
 
 def tree_workspace_size(B: int, T: int, Hq: int, Hkv: int, max_ctx_len: int, d: int, window: int) -> int:
-    """Bytes of device scratch attn_tree_paged needs for this shape (on the current device)."""
+    """Bytes of device scratch attn_tree_paged needs for this shape on the current device."""
     return int(lib().relbias_attn_tree_paged_workspace_size(B, T, Hq, Hkv, int(max_ctx_len), d, int(window)))
 
 
@@ -628,37 +657,44 @@ def attn_tree_paged(q, k_pages, v_pages, block_table, ctx_lens, tree_lens, depth
     (fills `lse` [B,Hq,T] fp32 when given); rows past tree_lens[b] are left as they were in
     `out` (allocated, uninitialised, if None).  `workspace`: a byte tensor of at least
     tree_workspace_size(...) bytes; allocated if None."""
-    _need(q.dim() == 4 and k_pages.dim() == 4 and v_pages.shape == k_pages.shape and block_table.dim() == 2,
+    _need(q.dim() == 4 and k_pages.dim() == 4 and block_table.dim() == 2,
           "q [B,T,Hq,d], pages [num_pages,page_size,Hkv,d], block_table [B,max_pages]")
-    B, T, Hq, d = q.shape
-    num_pages, page_size, Hkv, dk = k_pages.shape
+    B, T, Hq, d = shape = q.shape
+    num_pages, page_size, Hkv, dk = pool = k_pages.shape
+    max_pages, dtype, i32, f32 = block_table.shape[1], q.dtype, torch.int32, torch.float32
     _need(dk == d, "page head dim %d != q head dim %d" % (dk, d))
-    _need(q.dtype == k_pages.dtype == v_pages.dtype, "q and pages must share a dtype")
-    max_pages = block_table.shape[1]
-    _i32((B, max_pages), block_table=block_table)
-    _i32((B,), ctx_lens=ctx_lens, tree_lens=tree_lens)
-    _i32((B, T), depth=depth)
-    _i32((B, T, (T + 31) // 32), mask=mask)
-    _need(r.shape == (B, T, Hq) and r.dtype == torch.float32, "r must be fp32 [B,T,Hq]")
-    _need(w is None or (w.shape == (Hq, R) and w.dtype == torch.float32), "w must be fp32 [Hq,R]")
+    dev = _device_of(q, "q")
+    _dense(q, "q", dev, dtype, shape)
+    _dense(k_pages, "k_pages", dev, dtype, pool)
+    _dense(v_pages, "v_pages", dev, dtype, pool)
+    _dense(block_table, "block_table", dev, i32, (B, max_pages))
+    _dense(ctx_lens, "ctx_lens", dev, i32, (B,))
+    _dense(tree_lens, "tree_lens", dev, i32, (B,))
+    _dense(depth, "depth", dev, i32, (B, T))
+    _dense(mask, "mask", dev, i32, (B, T, (T + 31) // 32))
+    _dense(r, "r", dev, f32, (B, T, Hq))
+    if w is not None:
+        _dense(w, "w", dev, f32, (Hq, R))
     if out is None:
         out = torch.empty_like(q)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
-    _need(lse is None or (lse.shape == (B, Hq, T) and lse.dtype == torch.float32), "lse must be fp32 [B,Hq,T]")
-    _on_device(q, q=q, k_pages=k_pages, v_pages=v_pages, block_table=block_table, ctx_lens=ctx_lens,
-               tree_lens=tree_lens, depth=depth, mask=mask, r=r, w=w, out=out, lse=lse, workspace=workspace)
-    code = _dtype_code(q)
+    else:
+        _dense(out, "out", dev, dtype, shape)
+    if lse is not None:
+        _dense(lse, "lse", dev, f32, (B, Hq, T))
+    code, max_ctx_len, window = _dtype_code(q), int(max_ctx_len), int(window)
+    ws_bytes = 0
     if workspace is None:
-        with torch.cuda.device(q.device):
-            need = tree_workspace_size(B, T, Hq, Hkv, max_ctx_len, d, window)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    _call(lib().relbias_attn_tree_paged, q, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        ws_bytes = _on(dev, lib().relbias_attn_tree_paged_workspace_size, B, T, Hq, Hkv, max_ctx_len, d, window)
+        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace.get_device() == dev and workspace.is_contiguous(), "workspace must be dense, on q's device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _call(lib().relbias_attn_tree_paged, dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           block_table.data_ptr(), ctx_lens.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(), mask.data_ptr(),
           r.data_ptr(), None if w is None else w.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-          B, T, num_pages, page_size, max_pages, int(max_ctx_len), Hq, Hkv, d, int(window), int(R), float(scale),
-          int(temp_n0), code, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          B, T, num_pages, page_size, max_pages, max_ctx_len, Hq, Hkv, d, window, int(R),
+          1.0 / math.sqrt(d) if scale is None else float(scale), int(temp_n0), code,
+          workspace.data_ptr(), ws_bytes)
     return out
 
 
@@ -668,21 +704,21 @@ def kv_compact(k_pages, v_pages, block_table, ctx_lens, path, path_lens, stream=
     [num_pages,page_size,Hkv,d], or [layers,num_pages,page_size,Hkv,d] for all layers in one
     call (bf16 or fp32); block_table [B,max_pages], ctx_lens [B], path [B,A] (strictly
     increasing node indices), path_lens [B] int32; A <= 128."""
-    _need(k_pages.dim() in (4, 5) and v_pages.shape == k_pages.shape and v_pages.dtype == k_pages.dtype,
-          "pages [num_pages,page_size,Hkv,d] or [layers,num_pages,page_size,Hkv,d]")
-    _need(path.dim() == 2 and block_table.dim() == 2, "path [B,A], block_table [B,max_pages]")
+    _need(k_pages.dim() in (4, 5) and path.dim() == 2 and block_table.dim() == 2,
+          "pages [num_pages,page_size,Hkv,d] or [layers,num_pages,page_size,Hkv,d], path [B,A], block_table [B,max_pages]")
     B, A = path.shape
-    _i32((B, A), path=path)
-    _i32((B,), ctx_lens=ctx_lens, path_lens=path_lens)
-    _i32((B, block_table.shape[1]), block_table=block_table)
-    _on_device(k_pages, k_pages=k_pages, v_pages=v_pages, block_table=block_table, ctx_lens=ctx_lens, path=path,
-               path_lens=path_lens)
-    code = _dtype_code(k_pages)
-    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
-    num_pages, page_size, Hkv, d = k_pages.shape[-4:]
-    _call(lib().relbias_kv_compact, k_pages, stream, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-          ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), layers, B, A, num_pages, page_size,
-          block_table.shape[1], Hkv, d, code)
+    max_pages, pool, i32 = block_table.shape[1], k_pages.shape, torch.int32
+    num_pages, page_size, Hkv, d = pool[-4:]
+    dev = _device_of(k_pages, "k_pages")
+    _dense(k_pages, "k_pages", dev, k_pages.dtype, pool)
+    _dense(v_pages, "v_pages", dev, k_pages.dtype, pool)
+    _dense(block_table, "block_table", dev, i32, (B, max_pages))
+    _dense(ctx_lens, "ctx_lens", dev, i32, (B,))
+    _dense(path, "path", dev, i32, (B, A))
+    _dense(path_lens, "path_lens", dev, i32, (B,))
+    _call(lib().relbias_kv_compact, dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+          ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), pool[0] if len(pool) == 5 else 1, B, A,
+          num_pages, page_size, max_pages, Hkv, d, _dtype_code(k_pages))
 
 
 def device_status(reset: bool = True) -> int:

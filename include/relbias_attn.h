@@ -466,8 +466,8 @@ RELBIAS_API int relbias_kv_append(const void* q, const void* k, const void* v, c
  * tree, or before the window of its first node) may hold anything; the values of rows
  * inside that range must be finite, those of masked nodes included.
  * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; workspace of at
- * least relbias_attn_tree_paged_workspace_size(...) bytes, 16-byte aligned, whose contents on
- * entry do not matter.  Lengths out of range are clamped and page indices outside the pool
+ * least relbias_attn_tree_paged_workspace_size(...) bytes, 16-byte aligned, whose
+ * contents on entry do not matter.  Lengths out of range are clamped and page indices outside the pool
  * read zeros (RELBIAS_STATUS_BAD_LENGTH); a depth outside [0, T) is clamped
  * (RELBIAS_STATUS_BAD_TREE).
  */

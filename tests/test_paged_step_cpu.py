@@ -105,7 +105,7 @@ def _tree(lib, **kw):
     (dict(B=-1), ARG), (dict(Hq=7), ARG), (dict(R=-1), ARG), (dict(w=None), ARG), (dict(scale=0.0), ARG),
     (dict(dtype=5), ARG), (dict(dtype=ops.RELBIAS_FP32), UNSUPPORTED), (dict(T=129), UNSUPPORTED),
     (dict(d=96), UNSUPPORTED), (dict(Hq=34), UNSUPPORTED), (dict(page=24), ARG), (dict(max_ctx=129), ARG),
-    (dict(max_ctx=-1), ARG), (dict(q=None), ARG), (dict(mask=None), ARG), (dict(r=None), ARG), (dict(ws=None), ARG),
+    (dict(max_ctx=-1), ARG), (dict(q=None), ARG), (dict(mask=None), ARG), (dict(r=None), ARG), (dict(ws=None), ARG), (dict(ws=FAKE + 8), ARG),
     (dict(o=FAKE + 8), ARG), (dict(table=FAKE + 2), ARG), (dict(lse=FAKE + 1), ARG), (dict(B=65536), UNSUPPORTED)])
 def test_tree_attention_refuses(lib, kw, code):
     assert _tree(lib, **kw) == code
