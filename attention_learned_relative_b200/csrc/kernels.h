@@ -210,8 +210,8 @@ struct TreeAttnParams {
     int groups;                      // pairs of row tiles of a full tree
     int runs;                        // runs of a pair's tile stream
     int part_rows;                   // rows of a partial
-    int tab_bufs;                    // buffers of bias slices
-    bool cuttable;                   // some segment may have more than one key tile
+    int max_tiles;                   // key tiles of the longest segment there may be
+    int nq, nk, nv, tab_bufs;        // Q buffers, K and V stages, buffers of the stagers (set at the launch)
     int num_pages, page_size, max_pages, max_ctx;
     int box_rows;                    // rows of a K/V box: the largest power of two up to 128 that divides a page
     int window, R;

@@ -261,6 +261,8 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.temp_n0 = temp_n0 > 1 ? temp_n0 : 0;
     p.inv_log_n0 = temp_n0 > 1 ? static_cast<float>(1.0 / std::log(static_cast<double>(temp_n0))) : 0.0f;
     p.box_rows = std::min(128, page_size & -page_size);
+    if (static_cast<long long>(B) * Hkv * tree_max_tiles(T, max_ctx_len, p.window, 128) > INT32_MAX)
+        return fail(RELBIAS_ERR_UNSUPPORTED, "too many key tiles (%d sequences, %d heads)", B, Hkv);
     const TreeLaunch plan = tree_launch_plan(B, T, Hkv, p.G, max_ctx_len, p.window, d, dev.sms);
     if (ws_bytes < plan.bytes)
         return fail(RELBIAS_ERR_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes,
@@ -268,7 +270,7 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.groups = plan.groups;
     p.runs = plan.runs;
     p.part_rows = plan.part_rows;
-    p.cuttable = tree_max_tiles(T, max_ctx_len, p.window, p.box_rows) > 1;
+    p.max_tiles = tree_max_tiles(T, max_ctx_len, p.window, p.box_rows);
     p.cuts = static_cast<int4*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cut_bytes);
     CUtensorMap tq, tk, tv;

@@ -25,24 +25,34 @@
 // max, sum) that the combine kernel merges.  CTAs of different row pairs run the same
 // stream side by side, so a K/V tile comes from HBM once and from L2 for the others.
 //
-// Warp roles (384 threads):
-//   warps 0-3, 4-7  softmax and epilogue of slot 0, slot 1 (one row per thread)
-//   warp 8          TMA producer: Q per segment, K and V per key tile (2-stage rings); a key
-//                   tile is 128 / box_rows boxes, each inside one page, one lane per box
-//   warp 9          TMEM allocator, zeroing of dead V rows, tcgen05.mma issuer
-//   warps 10-11     bias stagers: the distances a key tile meets span 128 + T - 1 values, so
+// Warp roles (640 threads):
+//   warps 0-15      softmax and epilogue: slot = warp / 8, and within a slot two threads per
+//                   row, 64 key columns each (warps w and w + 4, the same tensor-memory lanes)
+//   warp 16         walks the run's segments and publishes them; TMA producer: Q per segment,
+//                   K and V per key tile; a key tile is 128 / box_rows boxes, each inside one
+//                   page, one lane per box
+//   warp 17         TMEM allocator, zeroing of dead V rows, tcgen05.mma issuer
+//   warps 18-19     bias stagers: the distances a key tile meets span 128 + T - 1 values, so
 //                   they copy that slice of the group's tables to shared memory tile by
-//                   tile (any R, and nothing for the tiles beyond R)
+//                   tile (any R, and nothing for the tiles beyond R; asynchronous copies, one
+//                   L2 latency per slice), and for tiles with tree keys the keys' positions
+//                   and the nodes' masks, aligned to the tile
 // Units are (key tile, slot) pairs, alternating between the slots through all segments of
 // the run; the MMA warp issues QK(u), then PV(u - 1).  Products of one thread run in issue
 // order, so QK(u) may overwrite the P of unit u - 2, and when S(u) is complete O of its slot
-// holds all earlier units.
-// Tensor memory: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D); P (bf16) over S.
+// holds all earlier units.  A slot's chain QK, softmax, PV, next QK sets the period of the
+// loop, not the products' rate, which is why a row's softmax is shared by two threads.
+// Tensor memory: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D); each half's P (bf16)
+// over the first half of its own columns of S.
 //
-// Masks.  Tiles that hold tree keys, or that reach past some row's window, are masked (and
-// given their bias) by a pass over S in tensor memory before the softmax reads it: one or
-// two tiles per segment.  Other tiles add their bias in registers, if any key is nearer
-// than R, and are never masked.
+// Softmax.  A thread takes its 64 columns of S twice, 32 at a time: for the maximum (adding
+// the bias on the way, and storing the sum back), and, once the row's two halves have met
+// and exchanged their maxima, for the weights.  The reference max of a row moves, and O is
+// rescaled, only when the max has grown by more than 2^8.
+// Masks.  Sixteen-column chunks that hold tree keys are masked, and given their bias, by a
+// pass over S in tensor memory before the softmax reads it.  Other chunks add their bias in
+// registers, if any key is nearer than R, and are masked by one compare per key only in
+// tiles that reach past some row's window.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,53 +66,105 @@ namespace relbias {
 namespace {
 
 constexpr int kTrM = 128, kTrN = 128;      // rows of a row tile, keys of a key tile
-constexpr int kTrStages = 2;               // K and V ring depth
-constexpr int kTrThreads = 384;
-constexpr int kTrSoftmaxRegs = 216, kTrOtherRegs = 72;
+constexpr int kTrThreads = 640, kTrSoftmaxWarps = 16;
+// 640 threads launch with 96 registers each; the split gives the same total.
+constexpr int kTrSoftmaxRegs = 104, kTrOtherRegs = 64;
 constexpr float kTrGrow = 8.0f;            // log2 units: O is rescaled when a row's max grows by more
 constexpr int kTrMinTiles = 1;             // least key tiles of a CTA's run
 constexpr int kTrRec = 4;                  // floats of a partial record beyond its output: max, sum, pad
+constexpr int kTrMaxStages = 4;            // of K, and of V
+constexpr int kTrLongSegment = 32;         // key tiles of a segment that counts as long
+constexpr int kTrEmuPer8 = 0;              // of eight pairs of exponentials, those taken on the FMA pipe
+constexpr int kTrSegs = 4;                 // published segments
 
 template <int D>
 struct TreeLayout {
     static constexpr int kTile = kTrM * D * 2;
-    static constexpr int kBox = kTrM * 128;               // 128 rows of 64 columns
-    static constexpr int kQ = 0;                          // two row tiles
-    static constexpr int kK = kQ + 2 * kTile;
-    static constexpr int kV = kK + kTrStages * kTile;
-    // Then the slots' (max, sum) exchange of one-row-tile segments, [parity][slot][row], the
-    // bars, one or two runs of key positions, and as many slices of the bias table.
-    static constexpr int kXch = kV + kTrStages * kTile;
-    static constexpr int kBars = kXch + 2 * 2 * kTrM * 8;
+    static constexpr int kBox = kTrM * 128;   // 128 rows of 64 columns
 };
 
-struct TreeBars {
+// A CTA's part of one (sequence, key/value head) segment.
+struct TreeSeg {
+    int b, g;
+    int ctx, n, lo, end;   // as in TreeSeq
+    int nt;                // key tiles of the whole segment
+    int tile0, ntiles;     // this part's (ntiles 0: the run is over)
+    int jbase;             // first row of the first one
+    int first_slice;       // first tile with a slice of the bias table; all later ones have one
+    int two;               // 1: two row tiles, 0: one whose key tiles the slots share
+    int per;               // key tiles of a run
+};
+
+// Shared memory besides the tiles and slices.
+struct TreeShared {
+    float2 xch[2][4][kTrM];         // (max, sum) of each row from each slot and half, by segment parity
+    float maxima[2][2][2][kTrM];    // [slot][tile parity][half]: a tile's row maxima
     uint64_t q_full[2], q_empty[2];
-    uint64_t k_full[kTrStages], k_empty[kTrStages], v_full[kTrStages], v_empty[kTrStages];
+    uint64_t k_full[kTrMaxStages], k_empty[kTrMaxStages], v_full[kTrMaxStages], v_empty[kTrMaxStages];
     uint64_t s_full[2], p_full[2], o_final[2], o_free;
+    uint64_t pair[8];               // the two warps of a slot's 32 rows meet
     uint64_t tab_full[2], tab_empty[2];
-    uint64_t xch, mma_done;
-    long long part[kTrThreads / 32];   // scratch of the schedule's scan
-    long long start_prefix;            // where this CTA's run starts: tiles before its first sequence,
-    int start_seq;                     // and that sequence
+    uint64_t seg_full[kTrSegs], seg_empty[kTrSegs];
+    uint64_t xch_bar, mma_done;
+    TreeSeg segs[kTrSegs];
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr int kTrBarBytes = (static_cast<int>(sizeof(TreeBars)) + 15) / 16 * 16;
+constexpr int kTrSharedBytes = (static_cast<int>(sizeof(TreeShared)) + 15) / 16 * 16;
 
 // Floats of a head's slice of the bias table: 128 + T - 1 distances, in a stride that is 4
 // modulo 32, so that eight heads at one depth meet eight different banks.
 __host__ __device__ constexpr int tree_tab_stride(int T) { return (kTrN + T - 1 + 31) / 32 * 32 + 4; }
 
-int tree_smem_need(int d, int G, int T, int bufs) {
-    const int bars = d == 64 ? TreeLayout<64>::kBars : TreeLayout<128>::kBars;
-    return bars + kTrBarBytes + bufs * (G * tree_tab_stride(T) + kTrN) * 4 + 1024;
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number (the sum with
+// 1.5 * 2^23 has it in its low bits) and |f| <= 1/2, 2^f by its Taylor polynomial of degree 6
+// in f ln 2 (the first term left out is below 1.3e-7 of 2^f, an ulp of fp32), n added to the
+// exponent.  x is at most a few units above 0; below -126 the result is 2^-126, which no
+// sum or bf16 weight next to the row's largest can see, so a masked key (x = -inf) is set
+// to 0 apart.
+__device__ __forceinline__ uint64_t tree_exp2(uint64_t x2) {
+    constexpr float kC[7] = {1.0f, 0.69314718f, 0.24022651f, 0.055504109f, 0.0096181291f, 0.0013333558f, 0.00015403530f};
+    float a, b;
+    f2_unpack(x2, a, b);
+    const uint64_t x = f2_pack(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+    const uint64_t y = f2_add(x, f2_pack(12582912.0f, 12582912.0f));
+    const uint64_t n = f2_add(y, f2_pack(-12582912.0f, -12582912.0f));
+    const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
+    uint64_t q = f2_pack(kC[6], kC[6]);
+#pragma unroll
+    for (int i = 5; i >= 0; --i) q = f2_fma(q, f, f2_pack(kC[i], kC[i]));
+    float qa, qb, ya, yb;
+    f2_unpack(q, qa, qb);
+    f2_unpack(y, ya, yb);
+    qa = __uint_as_float(__float_as_uint(qa) + (__float_as_uint(ya) << 23));
+    qb = __uint_as_float(__float_as_uint(qb) + (__float_as_uint(yb) << 23));
+    return f2_pack(a == -INFINITY ? 0.0f : qa, b == -INFINITY ? 0.0f : qb);
 }
-// Slices are double-buffered where they fit (all but the largest groups and trees at d 128).
-int tree_tab_bufs(int d, int G, int T) { return tree_smem_need(d, G, T, 2) <= 232448 ? 2 : 1; }
-int tree_smem_bytes(int d, int G, int T) {
+
+// A buffer of the stagers: masks of up to 128 nodes, four words each; key positions; a slice
+// per head.
+__host__ __device__ constexpr int tree_buf_bytes(int G, int T) {
+    return kMaxTree * 16 + kTrN * 4 + G * tree_tab_stride(T) * 4;
+}
+
+// Buffers and stages that fit: [Q tiles][K ring][V ring][shared][stager buffers].
+struct TreeSmem {
+    int nq, nk, nv, bufs, bytes;
+};
+TreeSmem tree_smem(int d, int G, int T, bool one_row_tile, bool long_segments) {
+    const int tile = kTrM * d * 2, most = 232448 - 1024 - kTrSharedBytes;
+    TreeSmem x{2, 2, 2, 2, 0};
+    // With one row tile a second Q buffer hides the load of the next segment's queries, a
+    // third V stage more of the cache's latency: the latter pays where segments are long.
+    if (one_row_tile && long_segments) x.nq = 1;
+    if (4 * tile + x.nq * tile + 2 * tree_buf_bytes(G, T) > most) x.bufs = 1;
+    auto fits = [&](int nk, int nv) { return (x.nq + nk + nv) * tile + x.bufs * tree_buf_bytes(G, T) <= most; };
+    if (fits(2, 3)) x.nv = 3;
+    if (fits(3, 3)) x.nk = 3;
+    if (fits(4, 4)) x.nk = x.nv = 4;
     // One CTA per SM: each allocates all of tensor memory.
-    return std::max(tree_smem_need(d, G, T, tree_tab_bufs(d, G, T)), 120 * 1024);
+    x.bytes = std::max((x.nq + x.nk + x.nv) * tile + kTrSharedBytes + x.bufs * tree_buf_bytes(G, T) + 1024, 120 * 1024);
+    return x;
 }
 
 // A sequence's lengths, clamped into range, and its key tiles.
@@ -130,20 +192,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeAttnParams& p, int ctx, in
     return s;
 }
 
-// A CTA's part of one (sequence, key/value head) segment.
-struct TreeSeg {
-    int b, g;
-    TreeSeq q;
-    int tile0, ntiles;   // its key tiles
-    int jbase;           // first row of the first one
-    int first_slice;     // first tile with a slice of the bias table; all later ones have one
-    bool two;            // two row tiles, or one whose key tiles the slots share
-};
-
-// Walks the segments of a CTA's run [pos, stop) of its row pair's tile stream.  Every role
-// has its own copy.  The next sequence's lengths are loaded one sequence ahead.
+// Walks the segments of a CTA's run [pos, stop) of its row pair's tile stream.  The next
+// sequence's lengths are loaded one sequence ahead.  (The host checks that a stream has
+// fewer than 2^31 tiles.)
 struct TreeWalk {
-    long long pos, stop;
+    int pos, stop, per;      // per: tiles of a run
     int b, g, off;           // current sequence, its next key/value head, next tile in that segment
     TreeSeq q;
     int next_ctx, next_n;
@@ -153,35 +206,75 @@ struct TreeWalk {
         next_ctx = __ldg(p.ctx_lens + x);
         next_n = __ldg(p.tree_lens + x);
     }
-    __device__ __forceinline__ void start(const TreeAttnParams& p, int seq, long long prefix, long long at,
-                                          long long end) {
-        pos = at, stop = end, b = seq;
-        q = tree_seq(p, __ldg(p.ctx_lens + b), __ldg(p.tree_lens + b));
-        fetch(p);
-        const long long rest = at - prefix;
-        g = static_cast<int>(rest / q.nt);
-        off = static_cast<int>(rest - static_cast<long long>(g) * q.nt);
+    // Finds the start of run number `run`, by a whole warp: the stream's length, then the
+    // sequence that holds the run's first tile.
+    __device__ __forceinline__ void start(const TreeAttnParams& p, int grp, int npt, int run, int lane) {
+        auto tiles_of = [&](int x, TreeSeq& s) {
+            s = tree_seq(p, __ldg(p.ctx_lens + x), __ldg(p.tree_lens + x));
+            if (s.bad && grp == 0 && run == 0) atomicOr(&g_status, kStatusBadLength);
+            return 2 * grp * npt < s.n ? s.nt * p.Hkv : 0;
+        };
+        int total = 0, mine = 0;   // mine: of this lane's sequence among the first 32
+        TreeSeq s{};
+        for (int x = lane; x < p.B; x += 32) {
+            TreeSeq y;
+            const int t = tiles_of(x, y);
+            if (x < 32) mine = t, s = y;
+            total += t;
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+        per = max((total + p.runs - 1) / p.runs, kTrMinTiles);
+        const long long at = static_cast<long long>(run) * per;
+        pos = static_cast<int>(min(at, static_cast<long long>(total)));
+        stop = min(total - pos, per) + pos;
+        if (pos >= stop) return;
+        for (int x0 = 0, prefix = 0;; x0 += 32) {
+            if (x0 > 0) mine = x0 + lane < p.B ? tiles_of(x0 + lane, s) : 0;
+            int scan = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, scan, o);
+                if (lane >= o) scan += up;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, pos < prefix + scan);
+            if (hit == 0) {
+                prefix += __shfl_sync(0xffffffffu, scan, 31);
+                continue;
+            }
+            const int w = __ffs(hit) - 1;
+            b = x0 + w;
+            const int rest = pos - prefix - __shfl_sync(0xffffffffu, scan - mine, w);
+            q.ctx = __shfl_sync(0xffffffffu, s.ctx, w);
+            q.n = __shfl_sync(0xffffffffu, s.n, w);
+            fetch(p);
+            q = tree_seq(p, q.ctx, q.n);
+            g = rest / q.nt;
+            off = rest - g * q.nt;
+            return;
+        }
     }
-    __device__ __forceinline__ bool next(const TreeAttnParams& p, int grp, int npt, TreeSeg& s) {
-        if (pos >= stop) return false;
+    __device__ __forceinline__ TreeSeg next(const TreeAttnParams& p, int grp, int npt) {
+        TreeSeg s{};
+        if (pos >= stop) return s;
         while (g == p.Hkv || 2 * grp * npt >= q.n) {   // the next sequence with rows of this pair
             ++b;
             g = 0;
             q = tree_seq(p, next_ctx, next_n);
             fetch(p);
         }
-        s.b = b, s.g = g, s.q = q;
+        s.b = b, s.g = g, s.ctx = q.ctx, s.n = q.n, s.lo = q.lo, s.end = q.end, s.nt = q.nt;
         s.tile0 = off;
-        s.ntiles = static_cast<int>(min(static_cast<long long>(q.nt - off), stop - pos));
+        s.ntiles = min(q.nt - off, stop - pos);
         s.jbase = q.base + off * kTrN;
         s.two = (2 * grp + 1) * npt < q.n;
         // A tile has a slice if it holds a prefix key nearer than R to a node of depth 0, or a
         // tree key.
         s.first_slice = min(max(0, (q.ctx - max(p.R, 1) + 1 - s.jbase) / kTrN), s.ntiles);
+        s.per = per;
         pos += s.ntiles;
         off = 0;
         ++g;
-        return true;
+        return s;
     }
 };
 
@@ -192,26 +285,26 @@ __device__ __forceinline__ int tree_depth(const TreeAttnParams& p, int b, int t,
     return min(max(d, 0), p.T - 1);
 }
 
+// The products of one unit, by one thread.  Only the address part of a descriptor (its low
+// 14 bits, in 16-byte steps) changes from step to step.
 template <int D>
-__device__ __forceinline__ void tree_issue_qk(bool leader, uint32_t d_tmem, uint32_t q_addr, uint32_t k_addr) {
+__device__ __forceinline__ void tree_issue_qk(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc) {
     const uint32_t idesc = idesc_bf16_f32(kTrM, kTrN, false, false);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk & 3) * 32 + (kk >> 2) * TreeLayout<D>::kBox;
-        const uint64_t a = smem_desc_sw128(q_addr + off, 16, 1024), b = smem_desc_sw128(k_addr + off, 16, 1024);
-        if (leader) umma_ss(d_tmem, a, b, idesc, kk > 0 ? 1u : 0u);
+        const uint64_t off = ((kk & 3) * 32 + (kk >> 2) * TreeLayout<D>::kBox) >> 4;
+        umma_ss(d_tmem, q_desc + off, k_desc + off, idesc, kk > 0 ? 1u : 0u);
     }
 }
 
 template <int D>
-__device__ __forceinline__ void tree_issue_pv(bool leader, uint32_t d_tmem, uint32_t p_tmem, uint32_t v_addr,
-                                              bool accumulate) {
+__device__ __forceinline__ void tree_issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc, bool accumulate) {
     const uint32_t idesc = idesc_bf16_f32(kTrM, D, false, true);
 #pragma unroll
-    for (int kk = 0; kk < kTrN / 16; ++kk) {
-        const uint64_t b = smem_desc_sw128(v_addr + kk * 16 * 128, TreeLayout<D>::kBox, 1024);
-        if (leader) umma_ts(d_tmem, p_tmem + kk * 8, b, idesc, (accumulate || kk > 0) ? 1u : 0u);
-    }
+    for (int kk = 0; kk < kTrN / 16; ++kk)
+        // P of keys 0-63 and 64-127: 32 columns each, 64 apart.
+        umma_ts(d_tmem, p_tmem + (kk & 3) * 8 + (kk >> 2) * 64, v_desc + ((kk * 16 * 128) >> 4), idesc,
+                (accumulate || kk > 0) ? 1u : 0u);
 }
 
 // Zero rows [first, last) of a key tile, by a warp, before the tensor cores read it.
@@ -226,38 +319,13 @@ __device__ __forceinline__ void tree_zero_rows(uint8_t* tile, int first, int las
     __syncwarp();
 }
 
+// Four bytes from global to shared memory, asynchronously, and the wait for a thread's own.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ bool tree_all(bool ok) { return __all_sync(0xffffffffu, ok); }
-
-// A softmax thread's row of a segment.
-struct TreeRow {
-    bool ok;
-    int t, dep;
-    float r;
-    uint32_t words[kMaxTree / 32];
-};
-
-__device__ __forceinline__ TreeRow tree_row(const TreeAttnParams& p, const TreeSeg& s, int tile, int ri, int npt) {
-    TreeRow x;
-    const int node = ri / p.G, h = s.g * p.G + ri - node * p.G;
-    x.t = tile * npt + node;
-    x.ok = node < npt && x.t < s.q.n;
-    const size_t at = static_cast<size_t>(s.b) * p.T + (x.ok ? x.t : 0);
-    x.r = x.ok ? __ldg(p.r + at * p.Hq + h) : 0.0f;
-    bool bad;
-    x.dep = tree_depth(p, s.b, x.ok ? x.t : 0, bad);
-    if (x.ok && bad) atomicOr(&g_status, kStatusBadTree);
-#pragma unroll
-    for (int k = 0; k < kMaxTree / 32; ++k) x.words[k] = k < p.words ? __ldg(p.mask + at * p.words + k) : 0u;
-    return x;
-}
-
-// Word k of a row's mask; words before the tree are set, words after it clear.
-__device__ __forceinline__ uint32_t tree_word(const TreeRow& x, int k) {
-    uint32_t w = k < 0 ? 0xffffffffu : 0u;
-#pragma unroll
-    for (int i = 0; i < kMaxTree / 32; ++i) w = k == i ? x.words[i] : w;
-    return w;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kTrThreads, 1)
@@ -270,119 +338,112 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    TreeBars* bars = reinterpret_cast<TreeBars*>(smem + L::kBars);
-    int* kpos = reinterpret_cast<int*>(smem + L::kBars + kTrBarBytes);
-    float* tabs = reinterpret_cast<float*>(kpos + p.tab_bufs * kTrN);
-    const int tstride = tree_tab_stride(p.T);
-    volatile int* abort_flag = &bars->abort_flag;
+    uint8_t* q_tiles = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* k_ring = q_tiles + p.nq * L::kTile;
+    uint8_t* v_ring = k_ring + p.nk * L::kTile;
+    TreeShared* sh = reinterpret_cast<TreeShared*>(v_ring + p.nv * L::kTile);
+    uint8_t* bufs = reinterpret_cast<uint8_t*>(sh) + kTrSharedBytes;
+    const int tstride = tree_tab_stride(p.T), buf_bytes = tree_buf_bytes(p.G, p.T);
+    volatile int* abort_flag = &sh->abort_flag;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bars->q_full[s], 1);
-            mbar_init(&bars->q_empty[s], 1);
-            mbar_init(&bars->s_full[s], 1);
-            mbar_init(&bars->p_full[s], 4);
-            mbar_init(&bars->o_final[s], 1);
-            mbar_init(&bars->tab_full[s], 2);
-            mbar_init(&bars->tab_empty[s], 8);
+            mbar_init(&sh->q_full[s], 1);
+            mbar_init(&sh->q_empty[s], 1);
+            mbar_init(&sh->s_full[s], 1);
+            mbar_init(&sh->p_full[s], 8);
+            mbar_init(&sh->o_final[s], 1);
+            mbar_init(&sh->tab_full[s], 2);
+            mbar_init(&sh->tab_empty[s], kTrSoftmaxWarps);
         }
-        for (int s = 0; s < kTrStages; ++s) {
-            mbar_init(&bars->k_full[s], 1);
-            mbar_init(&bars->k_empty[s], 1);
-            mbar_init(&bars->v_full[s], 1);
-            mbar_init(&bars->v_empty[s], 1);
+        for (int s = 0; s < kTrMaxStages; ++s) {
+            mbar_init(&sh->k_full[s], 1);
+            mbar_init(&sh->k_empty[s], 1);
+            mbar_init(&sh->v_full[s], 1);
+            mbar_init(&sh->v_empty[s], 1);
         }
-        mbar_init(&bars->o_free, 8);
-        mbar_init(&bars->xch, 8);
-        mbar_init(&bars->mma_done, 1);
-        bars->abort_flag = 0;
+        for (int s = 0; s < 8; ++s) mbar_init(&sh->pair[s], 2);
+        for (int s = 0; s < kTrSegs; ++s) {
+            mbar_init(&sh->seg_full[s], 1);
+            mbar_init(&sh->seg_empty[s], kTrSoftmaxWarps + 3);
+        }
+        mbar_init(&sh->o_free, kTrSoftmaxWarps);
+        mbar_init(&sh->xch_bar, kTrSoftmaxWarps);
+        mbar_init(&sh->mma_done, 1);
+        sh->abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 17) {
+        tmem_alloc(&sh->tmem_base, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    if (warp == 16 && lane == 0) {
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
     }
 
-    // The stream: total tiles of this row pair's segments, and where this CTA's run starts.
-    auto tiles_of = [&](int x) -> long long {
-        const TreeSeq q = tree_seq(p, __ldg(p.ctx_lens + x), __ldg(p.tree_lens + x));
-        if (q.bad && blockIdx.x == 0) atomicOr(&g_status, kStatusBadLength);
-        return 2 * grp * npt < q.n ? static_cast<long long>(q.nt) * p.Hkv : 0;
-    };
-    long long mine = 0;   // of this thread's sequence in the first chunk of the scan
-    long long total = 0;
-    for (int x = threadIdx.x; x < p.B; x += kTrThreads) {
-        const long long t = tiles_of(x);
-        if (x < kTrThreads) mine = t;
-        total += t;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) bars->part[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int x = 0; x < kTrThreads / 32; ++x) total += bars->part[x];
-    const long long per = max((total + p.runs - 1) / p.runs, static_cast<long long>(kTrMinTiles));
-    const long long pos = run * per, stop = min(total, pos + per);
-    if (pos >= stop) {   // nothing here
-        if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
-        return;
-    }
-    long long prefix = 0;
-    for (int x0 = 0; x0 < p.B; x0 += kTrThreads) {
-        if (x0 > 0) mine = x0 + static_cast<int>(threadIdx.x) < p.B ? tiles_of(x0 + threadIdx.x) : 0;
-        long long scan = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += up;
-        }
-        __syncthreads();   // the sums of the round before have been read
-        if (lane == 31) bars->part[warp] = scan;
-        __syncthreads();
-        long long before = prefix;
-        for (int x = 0; x < kTrThreads / 32; ++x) {
-            if (x < warp) before += bars->part[x];
-            prefix += bars->part[x];
-        }
-        before += scan - mine;
-        if (before <= pos && pos < before + mine) {
-            bars->start_seq = x0 + threadIdx.x;
-            bars->start_prefix = before;
-        }
-        if (prefix > pos) break;   // the same in every thread
-    }
-    if (warp == 9) {
-        tmem_alloc(&bars->tmem_base, 512);
-        tmem_relinquish();
-        tc_fence_before();
-    }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = bars->tmem_base;
-    TreeWalk walk;
-    walk.start(p, bars->start_seq, bars->start_prefix, pos, stop);
-    TreeSeg s;
+    const uint32_t tmem_base = sh->tmem_base;
 
-    if (warp >= 8) {
+    // Consumers of the published segments: wait for number i, and give it back.
+    auto seg_wait = [&](int i) { return tree_all(mbar_wait(&sh->seg_full[i % kTrSegs], (i / kTrSegs) & 1, abort_flag)); };
+    auto seg_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->seg_empty[i % kTrSegs]);
+    };
+
+    if (warp >= kTrSoftmaxWarps) {
         regs_decrease<kTrOtherRegs>();
-        if (warp == 8) {
-            // ------------------------------------------------------------ TMA producer
+        if (warp == 16) {
+            // ------------------------------------------------------------ schedule and TMA producer
             const bool leader = elect_one();
             const int nboxes = kTrN / p.box_rows;
+            TreeWalk walk;
+            walk.start(p, grp, npt, run, lane);
             bool ok = true;
-            int nkv = 0, nk = 0, nv = 0;   // key tiles; loads issued: number n goes to stage n % 2, phase n / 2
-            int nq[2] = {0, 0};            // loads of each Q buffer
-            for (int seg = 0; ok && walk.next(p, grp, npt, s); ++seg) {
+            int nk = 0, nv = 0, ks = 0, vs = 0, kph = 1, vph = 1;   // loads issued; next stages and their phases
+            int nq[2] = {0, 0};                                     // loads of each Q buffer
+            // A key tile's V is loaded after the next tile's K, the order in which they are used.
+            int v_page = 0, v_row = 0, v_head = -1;
+            auto load = [&](bool is_v, int page, int prow, int head) -> bool {
+                uint64_t* full = is_v ? &sh->v_full[vs] : &sh->k_full[ks];
+                if (!tree_all(mbar_wait(is_v ? &sh->v_empty[vs] : &sh->k_empty[ks], is_v ? vph : kph, abort_flag)))
+                    return false;
+                if (leader) mbar_arrive_expect_tx(full, L::kTile);
+                __syncwarp();
+                if (lane < nboxes) {
+                    uint8_t* dst = (is_v ? v_ring + vs * L::kTile : k_ring + ks * L::kTile) + lane * p.box_rows * 128;
+                    for (int bx = 0; bx < D / 64; ++bx)
+                        tma_load_4d(dst + bx * L::kBox, is_v ? &tm_v : &tm_k, full, bx * 64, head, prow, page);
+                }
+                __syncwarp();
+                if (is_v) {
+                    ++nv;
+                    if (++vs == p.nv) vs = 0, vph ^= 1;
+                } else {
+                    ++nk;
+                    if (++ks == p.nk) ks = 0, kph ^= 1;
+                }
+                return true;
+            };
+            for (int i = 0; ok; ++i) {
+                const TreeSeg s = walk.next(p, grp, npt);
+                if (!(ok = tree_all(mbar_wait(&sh->seg_empty[i % kTrSegs], ((i / kTrSegs) & 1) ^ 1, abort_flag)))) break;
+                if (lane == 0) {
+                    sh->segs[i % kTrSegs] = s;
+                    mbar_arrive(&sh->seg_full[i % kTrSegs]);
+                }
+                __syncwarp();
+                if (s.ntiles == 0) break;
                 // This lane's box of key tile t: its page (-1, which reads zeros, past the
                 // sequence's end or for an index outside the pool) and its row in the page.
                 auto lookup = [&](int t, int& page, int& prow) {
                     page = -1, prow = 0;
                     const int row = s.jbase + t * kTrN + lane * p.box_rows;
-                    if (t >= s.ntiles || lane >= nboxes || row >= s.q.end) return;
+                    if (t >= s.ntiles || lane >= nboxes || row >= s.end) return;
                     const int blk = row / p.page_size;
                     prow = row - blk * p.page_size;
                     page = __ldg(p.block_table + static_cast<size_t>(s.b) * p.max_pages + blk);
@@ -393,150 +454,168 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 };
                 int page, prow, next_page, next_row;
                 lookup(0, next_page, next_row);
-                // Two row tiles go to buffers 0 and 1; single ones alternate, so that a segment's
-                // queries arrive while the one before is still being read.
+                // Two row tiles go to buffers 0 and 1; single ones alternate where there are two, so
+                // that a segment's queries arrive while the one before is still being read.
                 for (int r = 0; r < (s.two ? 2 : 1); ++r) {
-                    const int buf = s.two ? r : seg & 1;
-                    if (!(ok = tree_all(mbar_wait(&bars->q_empty[buf], (nq[buf] & 1) ^ 1, abort_flag)))) break;
+                    const int buf = s.two ? r : p.nq == 2 ? i & 1 : 0;
+                    if (!(ok = tree_all(mbar_wait(&sh->q_empty[buf], (nq[buf] & 1) ^ 1, abort_flag)))) break;
                     if (leader) {
-                        mbar_arrive_expect_tx(&bars->q_full[buf], npt * p.G * 128 * (D / 64));
+                        mbar_arrive_expect_tx(&sh->q_full[buf], npt * p.G * 128 * (D / 64));
                         for (int bx = 0; bx < D / 64; ++bx)
-                            tma_load_4d(smem + L::kQ + buf * L::kTile + bx * L::kBox, &tm_q, &bars->q_full[buf],
-                                        bx * 64, s.g * p.G, (2 * grp + r) * npt, s.b);
+                            tma_load_4d(q_tiles + buf * L::kTile + bx * L::kBox, &tm_q, &sh->q_full[buf], bx * 64,
+                                        s.g * p.G, (2 * grp + r) * npt, s.b);
                     }
                     ++nq[buf];
                 }
-                for (int t = 0; ok && t < s.ntiles; ++t, ++nkv) {
-                    const int st = nkv & 1;
-                    const uint32_t ph = (nkv >> 1) & 1;
+                for (int t = 0; ok && t < s.ntiles; ++t) {
                     page = next_page, prow = next_row;
                     lookup(t + 1, next_page, next_row);
-                    for (int kv = 0; kv < 2; ++kv) {
-                        uint64_t* full = kv ? &bars->v_full[st] : &bars->k_full[st];
-                        if (!(ok = tree_all(
-                                  mbar_wait(kv ? &bars->v_empty[st] : &bars->k_empty[st], ph ^ 1, abort_flag))))
-                            break;
-                        if (leader) mbar_arrive_expect_tx(full, L::kTile);
-                        __syncwarp();
-                        if (lane < nboxes) {
-                            uint8_t* dst = smem + (kv ? L::kV : L::kK) + st * L::kTile + lane * p.box_rows * 128;
-                            for (int bx = 0; bx < D / 64; ++bx)
-                                tma_load_4d(dst + bx * L::kBox, kv ? &tm_v : &tm_k, full, bx * 64, s.g, prow, page);
-                        }
-                        __syncwarp();
-                        if (kv) ++nv; else ++nk;
-                    }
+                    if (!(ok = load(false, page, prow, s.g))) break;
+                    if (v_head >= 0 && !(ok = load(true, v_page, v_row, v_head))) break;
+                    v_page = page, v_row = prow, v_head = s.g;
                 }
             }
+            if (ok && v_head >= 0) load(true, v_page, v_row, v_head);
             // Drain, also after an abort: no copy may be in flight when the CTA exits.
             for (int x = 0; x < 2; ++x)
-                if (nq[x] > 0) mbar_drain_wait(&bars->q_full[x], (nq[x] - 1) & 1);
-            for (int n = max(0, nk - kTrStages); n < nk; ++n) mbar_drain_wait(&bars->k_full[n & 1], (n >> 1) & 1);
-            for (int n = max(0, nv - kTrStages); n < nv; ++n) mbar_drain_wait(&bars->v_full[n & 1], (n >> 1) & 1);
-        } else if (warp == 9) {
+                if (nq[x] > 0) mbar_drain_wait(&sh->q_full[x], (nq[x] - 1) & 1);
+            for (int n = max(0, nk - p.nk); n < nk; ++n) mbar_drain_wait(&sh->k_full[n % p.nk], (n / p.nk) & 1);
+            for (int n = max(0, nv - p.nv); n < nv; ++n) mbar_drain_wait(&sh->v_full[n % p.nv], (n / p.nv) & 1);
+        } else if (warp == 17) {
             // ------------------------------------------------------------ MMA issuer
+            // The whole warp runs the loop and waits; one thread issues.  Between two batches of
+            // products this warp's own work is what the tensor cores wait for, so it is short: no
+            // arrays, phases as bits.
             const bool leader = elect_one();
-            const uint32_t q_addr = smem_u32(smem + L::kQ), k_addr = smem_u32(smem + L::kK),
-                           v_addr = smem_u32(smem + L::kV);
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tiles), 16, 1024),
+                           k_desc = smem_desc_sw128(smem_u32(k_ring), 16, 1024),
+                           v_desc = smem_desc_sw128(smem_u32(v_ring), L::kBox, 1024);
+            constexpr uint32_t kStep = L::kTile >> 4;
             bool ok = true;
-            int nq[2] = {0, 0}, np[2] = {0, 0};   // uses of the Q buffers; P tiles taken from each slot
-            int nkv = 0, parity = 0;              // key tiles and units of earlier segments (units modulo 2)
-            // The unit whose PV is still to be issued.
-            struct {
-                bool any, opens, closes, first, accumulate, last;
-                int slot, tile, lo, end, j0;
-            } pv{};
+            uint32_t q_phase = 0, p_phase = 0;   // by Q buffer, by slot
+            uint32_t ks = 0, k_phase = 0, vs = 0, v_phase = 0, parity = 0;
+            // The unit whose PV is still to be issued (pv_slot 2: none), its tile's live rows, and
+            // whether it opens and closes its V stage and its segment's products.
+            uint32_t pv_slot = 2, pv_seg = 0;
+            int pv_lo = 0, pv_end = 0;
+            bool pv_opens = false, pv_closes = false, pv_adds = false, pv_last = false;
             // PV of the pending unit; the next unit's QK has been issued.
-            auto issue_pv = [&](int seg) -> bool {
-                const int st = pv.tile & 1;
-                if (pv.opens) {
-                    if (!tree_all(mbar_wait(&bars->v_full[st], (pv.tile >> 1) & 1, abort_flag))) return false;
+            auto issue_pv = [&]() -> bool {
+                if (pv_opens) {
+                    if (!tree_all(mbar_wait(&sh->v_full[vs], v_phase, abort_flag))) return false;
                     // Rows no node sees by position may hold anything, and a NaN times a zero
                     // weight is NaN: zero them before the first product reads them.
-                    uint8_t* vt = smem + L::kV + st * L::kTile;
-                    if (pv.end < pv.j0 + kTrN) tree_zero_rows<D>(vt, pv.end - pv.j0, kTrN, lane);
-                    if (pv.lo > pv.j0) tree_zero_rows<D>(vt, 0, pv.lo - pv.j0, lane);
+                    if (pv_end < kTrN) tree_zero_rows<D>(v_ring + vs * L::kTile, pv_end, kTrN, lane);
+                    if (pv_lo > 0) tree_zero_rows<D>(v_ring + vs * L::kTile, 0, pv_lo, lane);
+                    // A segment's first product overwrites O: all epilogues of the one before are done.
+                    if (pv_seg > 0 && !tree_all(mbar_wait(&sh->o_free, (pv_seg - 1) & 1, abort_flag))) return false;
                 }
-                if (!tree_all(mbar_wait(&bars->p_full[pv.slot], np[pv.slot] & 1, abort_flag))) return false;
-                ++np[pv.slot];
-                // A segment's first product overwrites O: all epilogues of the one before are done.
-                if (pv.first && seg > 0 && !tree_all(mbar_wait(&bars->o_free, (seg - 1) & 1, abort_flag))) return false;
+                if (!tree_all(mbar_wait(&sh->p_full[pv_slot], (p_phase >> pv_slot) & 1, abort_flag))) return false;
+                p_phase ^= 1u << pv_slot;
                 tc_fence_after();
-                tree_issue_pv<D>(leader, tmem_base + 256 + pv.slot * 128, tmem_base + pv.slot * 128,
-                                 v_addr + st * L::kTile, pv.accumulate);
-                if (leader && pv.closes) umma_commit(&bars->v_empty[st]);
-                if (leader && pv.last) umma_commit(&bars->o_final[pv.slot]);
+                if (leader) {
+                    tree_issue_pv<D>(tmem_base + 256 + pv_slot * 128, tmem_base + pv_slot * 128, v_desc + vs * kStep,
+                                     pv_adds);
+                    if (pv_closes) umma_commit(&sh->v_empty[vs]);
+                    if (pv_last) umma_commit(&sh->o_final[pv_slot]);
+                }
+                __syncwarp();
+                if (pv_closes && ++vs == static_cast<uint32_t>(p.nv)) vs = 0, v_phase ^= 1;
                 return true;
             };
-            int seg = 0;
-            for (; ok && walk.next(p, grp, npt, s); ++seg) {
-                const int units = s.two ? 2 * s.ntiles : s.ntiles;
-                for (int u = 0; ok && u < units; ++u) {
-                    const int ls = u & 1, slot = ls ^ parity, t = nkv + (s.two ? u >> 1 : u), st = t & 1;
-                    const int buf = s.two ? ls : seg & 1;
-                    const bool opens = !s.two || ls == 0, closes = !s.two || ls == 1;
-                    if (opens && !(ok = tree_all(mbar_wait(&bars->k_full[st], (t >> 1) & 1, abort_flag)))) break;
-                    if (u < (s.two ? 2 : 1) && !(ok = tree_all(mbar_wait(&bars->q_full[buf], nq[buf]++ & 1, abort_flag))))
-                        break;
+            for (int i = 0; ok; ++i) {
+                if (!(ok = seg_wait(i))) break;
+                const TreeSeg& s = sh->segs[i % kTrSegs];
+                const int ntiles = s.ntiles, two = s.two, units = two ? 2 * ntiles : ntiles;
+                int lo = s.lo - s.jbase, end = s.end - s.jbase;   // live rows, from the current tile's first
+                seg_done(i);
+                if (ntiles == 0) break;
+                for (int u = 0; u < units; ++u) {
+                    const uint32_t ls = u & 1, slot = ls ^ parity;
+                    const uint32_t buf = two ? ls : p.nq == 2 ? i & 1 : 0;
+                    const bool opens = !two || ls == 0, closes = !two || ls == 1;
+                    if (opens && !(ok = tree_all(mbar_wait(&sh->k_full[ks], k_phase, abort_flag)))) break;
+                    if (u <= two) {   // the unit reads its row tile for the first time
+                        if (!(ok = tree_all(mbar_wait(&sh->q_full[buf], (q_phase >> buf) & 1, abort_flag)))) break;
+                        q_phase ^= 1u << buf;
+                    }
                     tc_fence_after();
-                    tree_issue_qk<D>(leader, tmem_base + slot * 128, q_addr + buf * L::kTile, k_addr + st * L::kTile);
-                    if (leader) umma_commit(&bars->s_full[slot]);
-                    if (leader && closes) umma_commit(&bars->k_empty[st]);
-                    if (leader && u + (s.two ? 2 : 1) >= units) umma_commit(&bars->q_empty[buf]);
-                    if (pv.any && !(ok = issue_pv(pv.first && u == 0 ? seg - 1 : pv.first ? seg : 0))) break;
-                    pv = {true, opens, closes, u == 0, u >= 2, u + 2 >= units, slot, t,
-                          s.q.lo, s.q.end, s.jbase + (t - nkv) * kTrN};
+                    if (leader) {
+                        tree_issue_qk<D>(tmem_base + slot * 128, q_desc + buf * kStep, k_desc + ks * kStep);
+                        umma_commit(&sh->s_full[slot]);
+                        if (closes) umma_commit(&sh->k_empty[ks]);
+                        if (u + 1 + two >= units) umma_commit(&sh->q_empty[buf]);
+                    }
+                    __syncwarp();
+                    if (closes && ++ks == static_cast<uint32_t>(p.nk)) ks = 0, k_phase ^= 1;
+                    if (pv_slot < 2 && !(ok = issue_pv())) break;
+                    pv_slot = slot, pv_seg = u == 0 ? i : 0, pv_lo = lo, pv_end = end;
+                    pv_opens = opens, pv_closes = closes, pv_adds = u >= 2, pv_last = u + 2 >= units;
+                    if (closes) lo -= kTrN, end -= kTrN;
                 }
-                nkv += s.ntiles;
                 parity ^= units & 1;
             }
-            if (ok && pv.any) issue_pv(seg - 1);
+            if (ok && pv_slot < 2) issue_pv();
             // Drain: every product issued has finished before tensor memory is released.
-            if (leader) umma_commit(&bars->mma_done);
-            mbar_drain_wait(&bars->mma_done, 0);
+            if (leader) umma_commit(&sh->mma_done);
+            mbar_drain_wait(&sh->mma_done, 0);
         } else {
-            // ------------------------------------------------------------ bias stagers
-            const int x0 = threadIdx.x - 320;   // 0..63
+            // ------------------------------------------------------------ stagers
+            const int x0 = threadIdx.x - (kTrSoftmaxWarps + 2) * 32;   // 0..63
             const int width = kTrN + p.T - 1;
             int n = 0, cut = 0, cut_b = 0, cut_g = 0;
             bool ok = true;
-            while (ok && walk.next(p, grp, npt, s)) {
-                const int after = s.q.nt - s.tile0 - s.ntiles;
+            for (int i = 0; ok; ++i) {
+                if (!(ok = seg_wait(i))) break;
+                const TreeSeg s = sh->segs[i % kTrSegs];
+                seg_done(i);
+                if (s.ntiles == 0) break;
+                const int after = s.nt - s.tile0 - s.ntiles;
                 if (s.tile0 == 0 && after > 0) {
                     // The segment starts here and goes on in the next runs.
-                    cut = 1 + static_cast<int>((after + per - 1) / per);
+                    cut = 1 + (after + s.per - 1) / s.per;
                     cut_b = s.b, cut_g = s.g;
                 }
                 for (int t = s.first_slice; t < s.ntiles; ++t, ++n) {
                     const int buf = p.tab_bufs == 2 ? n & 1 : 0, use = p.tab_bufs == 2 ? n >> 1 : n;
-                    if (!(ok = tree_all(mbar_wait(&bars->tab_empty[buf], (use & 1) ^ 1, abort_flag)))) break;
+                    if (!(ok = tree_all(mbar_wait(&sh->tab_empty[buf], (use & 1) ^ 1, abort_flag)))) break;
+                    uint32_t* vis = reinterpret_cast<uint32_t*>(bufs + buf * buf_bytes);
+                    int* kpos = reinterpret_cast<int*>(vis + kMaxTree * 4);
+                    float* tab = reinterpret_cast<float*>(kpos + kTrN);
                     const int j0 = s.jbase + t * kTrN;
                     // The slice starts at the nearest key's distance from depth 0 (0 with tree keys).
-                    const int dlo = max(s.q.ctx - j0 - (kTrN - 1), 0);
-                    if (j0 + kTrN > s.q.ctx) {
-                        // Position of each key less ctx; dead keys lie far ahead of every node.
+                    const int dlo = max(s.ctx - j0 - (kTrN - 1), 0);
+                    if (j0 + kTrN > s.ctx) {
+                        // Position of each key less ctx; dead keys are in no mask.
                         for (int c = x0; c < kTrN; c += 64) {
-                            const int x = j0 + c - s.q.ctx;
+                            const int x = j0 + c - s.ctx;
                             bool bad;
-                            kpos[buf * kTrN + c] = x < 0 ? x : x < s.q.n ? tree_depth(p, s.b, x, bad) : INT_MAX / 2;
+                            kpos[c] = x < 0 ? x : x < s.n ? tree_depth(p, s.b, x, bad) : 0;
+                        }
+                        // Which keys each node of this row pair may see: all of the prefix, and by mask.
+                        const int first = 2 * grp * npt, nodes = min(2 * npt, s.n - first);
+                        for (int x = x0; x < 4 * nodes; x += 64) {
+                            const int bit = j0 + (x & 3) * 32 - s.ctx;   // the tree node of the word's bit 0
+                            const int* words = p.mask + (static_cast<size_t>(s.b) * p.T + first + (x >> 2)) * p.words;
+                            auto word = [&](int k) -> uint32_t {
+                                uint32_t w = k < 0 ? 0xffffffffu : k < p.words ? __ldg(words + k) : 0u;
+                                if (k >= 0 && s.n - 32 * k < 32) w = s.n > 32 * k ? w & ((1u << (s.n - 32 * k)) - 1u) : 0u;
+                                return w;
+                            };
+                            vis[x] = __funnelshift_r(word(bit >> 5), word((bit >> 5) + 1), bit & 31);
                         }
                     }
-                    float* tab = tabs + buf * p.G * tstride;
                     const float* src = p.w + static_cast<size_t>(s.g) * p.G * p.R + dlo;
-                    for (int x = x0; x < width; x += 64) {
-                        const bool in = dlo + x < p.R;
-                        for (int h0 = 0; h0 < p.G; h0 += 8) {   // eight loads in flight
-                            float v[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                v[e] = in && h0 + e < p.G ? __ldg(src + static_cast<size_t>(h0 + e) * p.R + x) : 0.0f;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (h0 + e < p.G) tab[(h0 + e) * tstride + x] = v[e];
+                    for (int h = 0; h < p.G; ++h, src += p.R)
+                        for (int x = x0; x < width; x += 64) {
+                            if (dlo + x < p.R)
+                                cp_async4(tab + h * tstride + x, src + x);
+                            else
+                                tab[h * tstride + x] = 0.0f;
                         }
-                    }
+                    cp_async_wait_all();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->tab_full[buf]);
+                    if (lane == 0) mbar_arrive(&sh->tab_full[buf]);
                 }
             }
             if (x0 == 0) p.cuts[blockIdx.x] = make_int4(cut, cut_b, cut_g, 0);
@@ -544,133 +623,153 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     } else {
         // ---------------------------------------------------------------- softmax / epilogue
         regs_increase<kTrSoftmaxRegs>();
-        const int slot = threadIdx.x >> 7;
-        const int ri = threadIdx.x & 127;
-        const uint32_t lane_off = static_cast<uint32_t>(ri & ~31) << 16;
-        const uint32_t s_tm = tmem_base + lane_off + slot * 128;
-        const int hh = ri % p.G;
+        const int slot = warp >> 3, half = (warp >> 2) & 1;
+        const int ri = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t s_tm = tmem_base + lane_off + slot * 128 + half * 64;   // this thread's 64 columns of S
+        uint64_t* pair = &sh->pair[slot * 4 + (warp & 3)];
+        const int node = ri / p.G, hh = ri - node * p.G;
         const int wlim = p.window > 0 ? p.window : INT_MAX;
         bool ok = true;
         int ns = 0, nslice = 0, parity = 0;    // S tiles of this slot; slices, and units (modulo 2), of earlier segments
-        int nf[2] = {0, 0}, nx = 0;            // finals of each slot; exchanges
-        bool more = walk.next(p, grp, npt, s);
-        TreeRow row = tree_row(p, s, 2 * grp + (s.two ? slot : 0), ri, npt);
-        while (ok && more) {
+        int nf[2] = {0, 0};                    // finals of each slot
+        // This thread's row of a segment: loaded one segment ahead.
+        struct {
+            int t, dep;
+            bool ok;
+            float r;
+        } row{};
+        auto load_row = [&](const TreeSeg& s, int part) {
+            row.t = (2 * grp + (s.two ? part : 0)) * npt + node;
+            row.ok = node < npt && row.t < s.n;
+            const size_t at = static_cast<size_t>(s.b) * p.T + (row.ok ? row.t : 0);
+            row.dep = __ldg(p.depth + at);
+            row.r = row.ok ? __ldg(p.r + at * p.Hq + s.g * p.G + hh) : 0.0f;
+        };
+        if ((ok = seg_wait(0)) && sh->segs[0].ntiles > 0) load_row(sh->segs[0], slot);
+        for (int i = 0; ok; ++i) {
+            const TreeSeg& s = sh->segs[i % kTrSegs];
+            const int ntiles = s.ntiles;
+            if (ntiles == 0) break;
+            const int two = s.two, ctx = s.ctx, first_slice = s.first_slice, jbase = s.jbase;
             const int ls = slot ^ parity;      // this slot's part: its row tile, or its half of the key tiles
-            const int h = s.g * p.G + hh;
+            const int t_node = row.t;
+            const bool row_ok = row.ok;
+            if (row_ok && (row.dep < 0 || row.dep >= p.T)) atomicOr(&g_status, kStatusBadTree);
+            const int dep = min(max(row.dep, 0), p.T - 1);
             const float rs = row.r * p.inv_scale;
             float c1 = p.scale_log2;
             // Context-length temperature: a row that sees n > temp_n0 keys (by position) has its
             // logits, content and bias, scaled by ln n / ln temp_n0.
             if (p.temp_n0 > 1) {
-                const int seen = min(s.q.ctx + row.dep + 1, wlim);
+                const int seen = min(ctx + dep + 1, wlim);
                 if (seen > p.temp_n0) c1 *= logf(static_cast<float>(seen)) * p.inv_log_n0;
             }
             const uint64_t c1x2 = f2_pack(c1, c1);
             float m_used = -INFINITY;   // running reference max, log2 units
-            uint64_t l2 = 0;            // running sum of the weights against it, in two lanes
-            const int t_first = s.two ? 0 : ls, t_step = s.two ? 1 : 2;
-            for (int t = t_first; t < s.ntiles; t += t_step, ++ns) {
-                const int j0 = s.jbase + t * kTrN;
-                const bool slice = t >= s.first_slice;
-                const bool tree = j0 + kTrN > s.q.ctx;
-                // Some key may be masked for some row.
-                const bool edge = tree || s.q.ctx + s.q.n - 1 - j0 >= wlim;
-                const int n = nslice + t - s.first_slice;
+            uint64_t l2 = 0;            // running sum of this half's weights against it, in two lanes
+            bool first = true;
+            for (int t = two ? 0 : ls; t < ntiles; t += two ? 1 : 2, ++ns) {
+                const int j0 = jbase + t * kTrN;
+                const bool slice = t >= first_slice;
+                const int n = nslice + t - first_slice;
                 const int buf = p.tab_bufs == 2 ? n & 1 : 0, use = p.tab_bufs == 2 ? n >> 1 : n;
-                const float* tab = tabs + (buf * p.G + hh) * tstride;
-                if (!(ok = tree_all(mbar_wait(&bars->s_full[slot], ns & 1, abort_flag)))) break;
-                if (slice && !(ok = tree_all(mbar_wait(&bars->tab_full[buf], use & 1, abort_flag)))) break;
+                const uint32_t* vis = reinterpret_cast<const uint32_t*>(bufs + buf * buf_bytes);
+                const int* kpos = reinterpret_cast<const int*>(vis + kMaxTree * 4);
+                const float* tab = reinterpret_cast<const float*>(kpos + kTrN) + hh * tstride;
+                if (!(ok = tree_all(mbar_wait(&sh->s_full[slot], ns & 1, abort_flag)))) break;
+                if (slice && !(ok = tree_all(mbar_wait(&sh->tab_full[buf], use & 1, abort_flag)))) break;
                 tc_fence_after();
-                if (edge) {
-                    // Bias and masks of an edge tile, 32 columns at a time, back into S.
-                    const int dlo = max(s.q.ctx - j0 - (kTrN - 1), 0);
+                const int own0 = ctx - j0 - half * 64;         // this half's first column with a tree key
+                const int dlo = max(ctx - j0 - (kTrN - 1), 0);   // the slice's first distance
+                if (own0 < 64) {
+                    // Bias and masks of the chunks with tree keys, back into S.
+                    const uint32_t* mine_vis = vis + (row_ok ? (t_node - 2 * grp * npt) * 4 : 0) + half * 2;
 #pragma unroll 1
-                    for (int cc = 0; cc < kTrN; cc += 32) {
-                        // Bits s0 .. s0 + 31 of the row's mask; keys before the tree are set.
-                        const int s0 = j0 + cc - s.q.ctx;
-                        uint32_t vis = __funnelshift_r(tree_word(row, s0 >> 5), tree_word(row, (s0 >> 5) + 1), s0 & 31);
-                        uint32_t sr[32];
-                        tmem_ld32(s_tm + cc, sr);
-                        int dist[32];
-                        if (tree) {
-                            const int4* kp = reinterpret_cast<const int4*>(kpos + buf * kTrN + cc);
+                    for (int cc = max(own0, 0) & ~15; cc < 64; cc += 16) {
+                        uint32_t see = mine_vis[cc >> 5] >> (cc & 16);
+                        uint32_t sr[16];
+                        tmem_ld16(s_tm + cc, sr);
+                        const int4* kp = reinterpret_cast<const int4*>(kpos + half * 64 + cc);
+                        float w[16];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int4 k4 = kp[e];
-                                dist[4 * e] = row.dep - k4.x, dist[4 * e + 1] = row.dep - k4.y;
-                                dist[4 * e + 2] = row.dep - k4.z, dist[4 * e + 3] = row.dep - k4.w;
+                        for (int e = 0; e < 4; ++e) {
+                            const int4 k4 = kp[e];
+                            const int ks[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) {
+                                const int dist = dep - ks[f];
+                                if (static_cast<unsigned>(dist) >= static_cast<unsigned>(wlim)) see &= ~(1u << (4 * e + f));
+                                w[4 * e + f] = tab[min(max(dist - dlo, 0), kTrN - 1 + p.T - 1)];
                             }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) dist[e] = row.dep - s0 - e;
                         }
+                        tmem_ld_wait_regs16(sr);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (static_cast<unsigned>(dist[e]) >= static_cast<unsigned>(wlim)) vis &= ~(1u << e);
-                        float w[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = 0.0f;
-                        if (slice) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) w[e] = tab[(vis >> e) & 1u ? dist[e] - dlo : 0];
-                        }
-                        tmem_ld_wait_regs(sr);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            sr[e] = (vis >> e) & 1u ? __float_as_uint(fmaf(rs, w[e], __uint_as_float(sr[e])))
+                        for (int e = 0; e < 16; ++e)
+                            sr[e] = (see >> e) & 1u ? __float_as_uint(fmaf(rs, w[e], __uint_as_float(sr[e])))
                                                     : 0xff800000u;
-                        tmem_st32(s_tm + cc, sr);
+                        tmem_st16(s_tm + cc, sr);
                         tmem_st_wait();
                         tmem_regs_keep16(sr);
-                        tmem_regs_keep16(sr + 16);
                     }
                 }
-                uint32_t sr[kTrN];
+                // The maximum, with the bias of the other chunks, and one compare per key where some
+                // row's window starts inside the tile (first column inside it: wcol).
+                const int wcol = wlim == INT_MAX ? INT_MIN : own0 + dep - wlim + 1;
+                const bool cuts_in = __any_sync(0xffffffffu, wcol > 0);
+                float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int cc = 0; cc < 64; cc += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(s_tm + cc, x);
+                    tmem_ld_wait_regs(x);
+                    if ((slice || cuts_in) && cc + 16 <= own0) {
+                        const float* w = tab + dep + own0 - dlo - cc;   // a prefix key's distance is dep + ctx less its row
 #pragma unroll
-                for (int c = 0; c < kTrN; c += 32) tmem_ld32(s_tm + c, sr + c);
-                tmem_ld_wait_regs(sr);
+                        for (int h = 0; h < 32; h += 16) {
+                            if (cc + h + 16 <= own0) {
+                                if (slice) {
 #pragma unroll
-                for (int c = 32; c < kTrN; c += 32) tmem_regs_fence(sr + c);
-                float x[kTrN];
+                                    for (int c = h; c < h + 16; ++c)
+                                        x[c] = __float_as_uint(fmaf(rs, w[-c], __uint_as_float(x[c])));
+                                }
+                                if (cuts_in) {
 #pragma unroll
-                for (int c = 0; c < kTrN; ++c) x[c] = __uint_as_float(sr[c]);
-                if (slice && !edge) {
-                    // Key c lies dep + 127 - c entries into the slice.
-                    const float* w = tab + row.dep + (kTrN - 1);
-#pragma unroll
-                    for (int c = 0; c < kTrN; ++c) x[c] = fmaf(rs, w[-c], x[c]);
-                }
-                if (slice) {
-                    // Eight arrivals free a slice: one per reading warp, two if only a slot's four read.
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bars->tab_empty[buf]);
-                        if (!s.two) mbar_arrive(&bars->tab_empty[buf]);
+                                    for (int c = h; c < h + 16; ++c) x[c] = cc + c < wcol ? 0xff800000u : x[c];
+                                }
+                            }
+                        }
+                        tmem_st32(s_tm + cc, x);
+                        tmem_st_wait();
+                        tmem_regs_keep16(x);
+                        tmem_regs_keep16(x + 16);
                     }
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mc[e] = fmax3f(mc[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
                 }
-                float mc[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mc[e] = fmaxf(x[2 * e], x[2 * e + 1]);
-#pragma unroll
-                for (int c = 16; c < kTrN; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mc[e] = fmax3f(mc[e], x[c + 2 * e], x[c + 2 * e + 1]);
-                const float mx =
-                    fmaxf(fmax3f(mc[0], mc[1], mc[2]), fmax3f(fmax3f(mc[3], mc[4], mc[5]), mc[6], mc[7])) * c1;
-                if (t == t_first) {
-                    m_used = mx;
-                } else if (__any_sync(0xffffffffu, mx > m_used + kTrGrow)) {
-                    // Some row's max grew past the slack (or is its first): what has been summed
-                    // is scaled to the new reference.
-                    const float m_new = mx > m_used + kTrGrow ? mx : m_used;
-                    const float alpha = m_used == -INFINITY ? 0.0f : ex2_approx(m_used - m_new);
-                    m_used = m_new;
+                const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+                sh->maxima[slot][ns & 1][half][ri] = mx;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pair);
+                if (!(ok = tree_all(mbar_wait(pair, ns & 1, abort_flag)))) break;
+                const float top = fmaxf(mx, sh->maxima[slot][ns & 1][half ^ 1][ri]) * c1;
+                if (first) {
+                    m_used = top;
+                    first = false;
+                } else if (__any_sync(0xffffffffu, top > m_used + kTrGrow)) {
+                    // Some row's max grew past the slack (or is its first): what has been summed is
+                    // scaled to the new reference, each half of the row's threads its half of O.
+                    const bool grow = top > m_used + kTrGrow;
+                    const float alpha = !grow ? 1.0f : m_used == -INFINITY ? 0.0f : ex2_approx(m_used - top);
+                    m_used = grow ? top : m_used;
                     l2 = f2_mul(l2, f2_pack(alpha, alpha));
-                    const uint32_t o_tm = tmem_base + lane_off + 256 + slot * 128;
+                    const uint32_t o_tm = tmem_base + lane_off + 256 + slot * 128 + half * (D / 2);
                     uint32_t ob[32];
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; c += 32) {
                         tmem_ld32(o_tm + c, ob);
                         tmem_ld_wait_regs(ob);
 #pragma unroll
@@ -683,128 +782,146 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 }
                 const float mb = m_used == -INFINITY ? 0.0f : m_used;
                 const uint64_t nm2 = f2_pack(-mb, -mb);
-                uint64_t acc[4] = {0, 0, 0, 0};
-                uint32_t pk[kTrN / 2];
+                uint64_t acc[2] = {0, 0};
+#pragma unroll 1
+                for (int cc = 0; cc < 64; cc += 32) {
+                    uint32_t x[32], pk[16];
+                    tmem_ld32(s_tm + cc, x);
+                    tmem_ld_wait_regs(x);
 #pragma unroll
-                for (int c = 0; c < kTrN; c += 2) {
-                    float x0, x1;
-                    f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), c1x2, nm2), x0, x1);
-                    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                    acc[(c >> 1) & 3] = f2_add(acc[(c >> 1) & 3], f2_pack(p0, p1));
-                    // Weights are rounded to bf16 for the tensor cores (2^-8 of each at most, while
-                    // their sum stays in fp32).
-                    pk[c / 2] = pack_bf16x2(p0, p1);
+                    for (int c = 0; c < 32; c += 2) {
+                        const uint64_t x2 =
+                            f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), c1x2, nm2);
+                        float p0, p1;
+                        if (((c >> 1) & 7) < kTrEmuPer8) {
+                            f2_unpack(tree_exp2(x2), p0, p1);
+                        } else {
+                            float x0, x1;
+                            f2_unpack(x2, x0, x1);
+                            p0 = ex2_approx(x0);
+                            p1 = ex2_approx(x1);
+                        }
+                        acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
+                        // Weights are rounded to bf16 for the tensor cores (2^-8 of each at most,
+                        // while their sum stays in fp32).
+                        pk[c / 2] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16(s_tm + cc / 2, pk);   // over columns of S that have been read
+                    tmem_st_wait();
+                    tmem_regs_keep16(pk);
                 }
-                l2 = f2_add(l2, f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])));
-                tmem_st32(s_tm, pk);
-                tmem_st32(s_tm + 32, pk + 32);
-                tmem_st_wait();
-#pragma unroll
-                for (int c = 0; c < kTrN / 2; c += 16) tmem_regs_keep16(pk + c);
+                l2 = f2_add(l2, f2_add(acc[0], acc[1]));
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[slot]);
+                if (lane == 0) {
+                    mbar_arrive(&sh->p_full[slot]);
+                    // Sixteen arrivals free a slice: one per reading warp, two if only a slot's eight read.
+                    if (slice) {
+                        mbar_arrive(&sh->tab_empty[buf]);
+                        if (!two) mbar_arrive(&sh->tab_empty[buf]);
+                    }
+                }
             }
             if (!ok) break;
 
-            // The next segment's row is fetched while this one's last products run.
-            const TreeSeg cur = s;
-            const TreeRow mine = row;
-            const int units = cur.two ? 2 * cur.ntiles : cur.ntiles;
-            nslice += cur.ntiles - cur.first_slice;
-            parity ^= units & 1;
-            more = walk.next(p, grp, npt, s);
-            if (more) row = tree_row(p, s, 2 * grp + (s.two ? slot ^ parity : 0), ri, npt);
-
-            // Epilogue.  Two row tiles: each slot writes its own rows.  One: both slots hold a
-            // part of every row, in the same tensor-memory lanes; they exchange their maxima and
-            // sums through shared memory and write half of the columns each.
+            // Epilogue.  The threads exchange their maxima and sums: the two halves of a row have
+            // one max and two sums; with one row tile the slots' parts of a row, in the same
+            // tensor-memory lanes, also have two maxima.  Each thread then writes a half (two row
+            // tiles) or a quarter of its row's columns.
+            const int units = two ? 2 * ntiles : ntiles;
+            // The next segment's row is on its way meanwhile.
+            if (!(ok = seg_wait(i + 1))) break;
+            if (sh->segs[(i + 1) % kTrSegs].ntiles > 0)
+                load_row(sh->segs[(i + 1) % kTrSegs], slot ^ parity ^ (units & 1));
             float la, lb;
             f2_unpack(l2, la, lb);
-            float l = la + lb, m = m_used;
+            float2* xch = sh->xch[i & 1][0];
+            xch[(slot * 2 + half) * kTrM + ri] = make_float2(m_used, la + lb);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->xch_bar);
+            if (!(ok = tree_all(mbar_wait(&sh->xch_bar, i & 1, abort_flag)))) break;
+            float m = m_used;
+            float l = xch[slot * 2 * kTrM + ri].y + xch[(slot * 2 + 1) * kTrM + ri].y;
             float a_own = 1.0f, a_other = 0.0f;   // scales of the slots' O
-            if (!cur.two) {
-                float2* xch = reinterpret_cast<float2*>(smem + L::kXch) + (nx & 1) * 2 * kTrM;
-                xch[slot * kTrM + ri] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->xch);
-                if (!(ok = tree_all(mbar_wait(&bars->xch, nx & 1, abort_flag)))) break;
-                ++nx;
-                const float2 y = xch[(slot ^ 1) * kTrM + ri];
-                const float top = fmaxf(m, y.x);
+            if (!two) {
+                const float mo = xch[(slot ^ 1) * 2 * kTrM + ri].x;
+                const float lo = xch[(slot ^ 1) * 2 * kTrM + ri].y + xch[((slot ^ 1) * 2 + 1) * kTrM + ri].y;
+                const float top = fmaxf(m, mo);
                 a_own = m == -INFINITY ? 0.0f : ex2_approx(m - top);
-                a_other = y.x == -INFINITY ? 0.0f : ex2_approx(y.x - top);
-                l = l * a_own + y.y * a_other;
+                a_other = mo == -INFINITY ? 0.0f : ex2_approx(mo - top);
+                l = l * a_own + lo * a_other;
                 m = top;
             }
             // Which slots' O hold something, and are waited for.
-            const bool own = cur.two || ls == 0 || units > 1, other = !cur.two && (ls == 1 || units > 1);
-            if (own && !(ok = tree_all(mbar_wait(&bars->o_final[slot], nf[slot] & 1, abort_flag)))) break;
-            if (other && !(ok = tree_all(mbar_wait(&bars->o_final[slot ^ 1], nf[slot ^ 1] & 1, abort_flag)))) break;
-            if (cur.two || ls == 0 || units > 1) ++nf[slot];
-            if (cur.two || ls == 1 || units > 1) ++nf[slot ^ 1];
+            const bool own = two || ls == 0 || units > 1, other = !two && (ls == 1 || units > 1);
+            if (own && !(ok = tree_all(mbar_wait(&sh->o_final[slot], nf[slot] & 1, abort_flag)))) break;
+            if (other && !(ok = tree_all(mbar_wait(&sh->o_final[slot ^ 1], nf[slot ^ 1] & 1, abort_flag)))) break;
+            if (own) ++nf[slot];
+            if (two || ls == 1 || units > 1) ++nf[slot ^ 1];
             tc_fence_after();
-            const bool left = cur.tile0 > 0, right = cur.tile0 + cur.ntiles < cur.q.nt;
-            const bool direct = !left && !right;
+            const bool left = s.tile0 > 0, direct = !left && ntiles == s.nt;
             if (direct) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 a_own *= inv;
                 a_other *= inv;
             }
-            const size_t orow = (static_cast<size_t>(cur.b) * p.T + mine.t) * p.Hq + h;
+            const int h = s.g * p.G + hh;
+            const size_t orow = (static_cast<size_t>(s.b) * p.T + t_node) * p.Hq + h;
             // A run's first cut segment goes to its partial 0 if it comes from the run before, else to 1.
             float* rec = p.part + (static_cast<size_t>(blockIdx.x * 2 + (left ? 0 : 1)) * p.part_rows +
-                                   (cur.two ? ls * kTrM : 0) + ri) * (D + kTrRec);
+                                   (two ? ls * kTrM : 0) + ri) * (D + kTrRec);
             const uint32_t o_tm = tmem_base + lane_off + 256;
-            const int c_lo = cur.two ? 0 : slot * (D / 2), c_hi = cur.two ? D : c_lo + D / 2;
+            const int part = two ? half : slot * 2 + half, width = two ? D / 2 : D / 4;
 #pragma unroll 1
-            for (int c = c_lo; c < c_hi; c += 32) {
-                uint32_t y[32];
+            for (int c = part * width; c < (part + 1) * width; c += 32) {
+                // 32 columns; of a one-row-tile segment at d 64 a thread has 16, and takes its
+                // neighbour's along unwritten.
+                const int cols = min(width, 32);
+                uint32_t y[32], z[32];
+                tmem_ld32(o_tm + slot * 128 + c, y);
+                tmem_ld32(o_tm + (slot ^ 1) * 128 + c, z);
+                tmem_ld_wait_regs(y);
+                tmem_regs_fence(z);
                 float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-                if (own) {
-                    tmem_ld32(o_tm + slot * 128 + c, y);
-                    tmem_ld_wait_regs(y);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(y[e]) * a_own;
+                for (int e = 0; e < 32; ++e) {
+                    v[e] = own ? __uint_as_float(y[e]) * a_own : 0.0f;
+                    v[e] = other ? fmaf(__uint_as_float(z[e]), a_other, v[e]) : v[e];
                 }
-                if (other) {
-                    tmem_ld32(o_tm + (slot ^ 1) * 128 + c, y);
-                    tmem_ld_wait_regs(y);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(y[e]), a_other, v[e]);
-                }
-                if (mine.ok) {
+                if (row_ok) {
                     if (direct) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
-                            st_global_v4(p.o + orow * D + c + e, pack_bf16x2(v[e], v[e + 1]),
-                                         pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]),
-                                         pack_bf16x2(v[e + 6], v[e + 7]));
+                            if (e < cols)
+                                st_global_v4(p.o + orow * D + c + e, pack_bf16x2(v[e], v[e + 1]),
+                                             pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]),
+                                             pack_bf16x2(v[e + 6], v[e + 7]));
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(rec + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                            if (e < cols)
+                                *reinterpret_cast<float4*>(rec + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
             }
-            if (mine.ok && (cur.two || slot == 0)) {
+            if (row_ok && part == 0) {
                 if (!direct) {
                     *reinterpret_cast<float2*>(rec + D) = make_float2(m, l);
                 } else if (p.lse != nullptr) {
-                    p.lse[(static_cast<size_t>(cur.b) * p.Hq + h) * p.T + mine.t] =
+                    p.lse[(static_cast<size_t>(s.b) * p.Hq + h) * p.T + t_node] =
                         l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 }
             }
+            nslice += ntiles - first_slice;
+            parity ^= units & 1;
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->o_free);
+            seg_done(i);
+            if (lane == 0) mbar_arrive(&sh->o_free);
         }
     }
 
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
     }
@@ -859,15 +976,15 @@ __global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(cons
 template <int D>
 cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeAttnParams p,
                         cudaStream_t stream) {
-    const int smem = tree_smem_bytes(D, p.G, p.T);
-    p.tab_bufs = tree_tab_bufs(D, p.G, p.T);
+    const TreeSmem sm = tree_smem(D, p.G, p.T, p.part_rows == kTrM, p.max_tiles >= kTrLongSegment);
+    p.nq = sm.nq, p.nk = sm.nk, p.nv = sm.nv, p.tab_bufs = sm.bufs;
     cudaError_t e =
-        cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm.bytes);
     if (e != cudaSuccess) return e;
     const int ctas = p.runs * p.groups;
-    tree_attn_kernel<D><<<ctas, kTrThreads, smem, stream>>>(tq, tk, tv, p);
+    tree_attn_kernel<D><<<ctas, kTrThreads, sm.bytes, stream>>>(tq, tk, tv, p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !p.cuttable) return e;
+    if (e != cudaSuccess || p.max_tiles == 1) return e;   // a segment of one tile is never cut
     const int rows = p.part_rows > kTrM ? p.part_rows : p.T * p.G;
     tree_combine_kernel<D><<<dim3((rows + kTrCombineWarps - 1) / kTrCombineWarps, ctas), kTrCombineWarps * 32, 0,
                              stream>>>(p);
