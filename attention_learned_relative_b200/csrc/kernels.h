@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstdint>
+
 namespace relbias {
 
 // bf16 tcgen05 prefill (prefill_sm100.cu).
@@ -213,6 +215,10 @@ struct TreeAttnParams {
     int max_tiles;                   // key tiles of the longest segment there may be
     int nq, nk, nv, tab_bufs;        // Q buffers, K and V stages, buffers of the stagers (set at the launch)
     int num_pages, page_size, max_pages, max_ctx;
+    // x / page_size = x * page_mul >> page_shift for 0 <= x < 2^31
+    uint64_t page_mul;
+    int page_shift;
+    bool w_bulk;                     // every row of w starts on a 16-byte boundary
     int box_rows;                    // rows of a K/V box: the largest power of two up to 128 that divides a page
     int window, R;
     float scale_log2, inv_scale;

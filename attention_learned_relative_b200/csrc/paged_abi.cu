@@ -261,6 +261,14 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.temp_n0 = temp_n0 > 1 ? temp_n0 : 0;
     p.inv_log_n0 = temp_n0 > 1 ? static_cast<float>(1.0 / std::log(static_cast<double>(temp_n0))) : 0.0f;
     p.box_rows = std::min(128, page_size & -page_size);
+    // Division by an invariant: with s = ceil(log2 page_size), m = ceil(2^(31 + s) / page_size)
+    // exceeds the quotient by less than 2^s / page_size units of 2^-(31 + s), which cannot reach
+    // the next whole number for x < 2^31.
+    int log2 = 0;
+    while ((1LL << log2) < page_size) ++log2;
+    p.page_shift = 31 + log2;
+    p.page_mul = ((1ull << p.page_shift) + page_size - 1) / page_size;
+    p.w_bulk = R % 4 == 0 && aligned16(w);
     if (static_cast<long long>(B) * Hkv * tree_max_tiles(T, max_ctx_len, p.window, 128) > INT32_MAX)
         return fail(RELBIAS_ERR_UNSUPPORTED, "too many key tiles (%d sequences, %d heads)", B, Hkv);
     const TreeLaunch plan = tree_launch_plan(B, T, Hkv, p.G, max_ctx_len, p.window, d, dev.sms);

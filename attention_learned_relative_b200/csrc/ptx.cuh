@@ -46,6 +46,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
                  : "memory");
 }
+// Bytes of copies the current phase also waits for; the arrival itself comes later.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
 // try_wait suspends the waiting thread for a system-dependent time, so waits do not
 // spin through the issue slots of the warps doing the work.  No explicit suspend-time
 // hint is given: on B200 every hint tried (20 ns to 200 us) woke waiters later after

@@ -34,9 +34,9 @@
 //   warp 17         TMEM allocator, zeroing of dead V rows, tcgen05.mma issuer
 //   warps 18-19     bias stagers: the distances a key tile meets span 128 + T - 1 values, so
 //                   they copy that slice of the group's tables to shared memory tile by
-//                   tile (any R, and nothing for the tiles beyond R; asynchronous copies, one
-//                   L2 latency per slice), and for tiles with tree keys the keys' positions
-//                   and the nodes' masks, aligned to the tile
+//                   tile (any R, and nothing for the tiles beyond R; one bulk copy per head),
+//                   and for tiles with tree keys the keys' positions and the nodes' masks,
+//                   aligned to the tile
 // Units are (key tile, slot) pairs, alternating between the slots through all segments of
 // the run; the MMA warp issues QK(u), then PV(u - 1).  Products of one thread run in issue
 // order, so QK(u) may overwrite the P of unit u - 2, and when S(u) is complete O of its slot
@@ -112,8 +112,9 @@ struct TreeShared {
 };
 constexpr int kTrSharedBytes = (static_cast<int>(sizeof(TreeShared)) + 15) / 16 * 16;
 
-// Floats of a head's slice of the bias table: 128 + T - 1 distances, in a stride that is 4
-// modulo 32, so that eight heads at one depth meet eight different banks.
+// Floats of a head's slice of the bias table: 128 + T - 1 distances and up to 3 before them (a
+// slice starts on a 16-byte boundary of its table row), in a stride that is 4 modulo 32, so
+// that eight heads at one depth meet eight different banks.
 __host__ __device__ constexpr int tree_tab_stride(int T) { return (kTrN + T - 1 + 31) / 32 * 32 + 4; }
 
 // 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number (the sum with
@@ -187,7 +188,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeAttnParams& p, int ctx, in
     }
     s.end = s.ctx + s.n;
     s.lo = p.window > 0 ? max(0, s.ctx - p.window + 1) : 0;
-    s.base = s.lo / p.box_rows * p.box_rows;
+    s.base = s.lo & -p.box_rows;   // a power of two
     s.nt = s.n > 0 ? (s.end - s.base + kTrN - 1) / kTrN : 0;
     return s;
 }
@@ -319,11 +320,36 @@ __device__ __forceinline__ void tree_zero_rows(uint8_t* tile, int first, int las
     __syncwarp();
 }
 
+// A run of 16-byte units from global to shared memory, signalled on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 // Four bytes from global to shared memory, asynchronously, and the wait for a thread's own.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Piece (lane & 3) of rows (lane & ~3) + e, e < 4, from four pieces of each lane's own row.
+__device__ __forceinline__ void tree_transpose4(uint4 (&u)[4], int lane) {
+    auto trade = [&](uint32_t& lo, uint32_t& hi, int m) {   // lo: index bit m clear, hi: set
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, (lane & m) ? lo : hi, m);
+        if (lane & m) lo = y; else hi = y;
+    };
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!(k & m)) {
+                trade(u[k].x, u[k | m].x, m);
+                trade(u[k].y, u[k | m].y, m);
+                trade(u[k].z, u[k | m].z, m);
+                trade(u[k].w, u[k | m].w, m);
+            }
+}
 
 __device__ __forceinline__ bool tree_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
@@ -444,7 +470,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     page = -1, prow = 0;
                     const int row = s.jbase + t * kTrN + lane * p.box_rows;
                     if (t >= s.ntiles || lane >= nboxes || row >= s.end) return;
-                    const int blk = row / p.page_size;
+                    const int blk = static_cast<int>(static_cast<uint64_t>(row) * p.page_mul >> p.page_shift);
                     prow = row - blk * p.page_size;
                     page = __ldg(p.block_table + static_cast<size_t>(s.b) * p.max_pages + blk);
                     if (page < 0 || page >= p.num_pages) {
@@ -562,7 +588,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         } else {
             // ------------------------------------------------------------ stagers
             const int x0 = threadIdx.x - (kTrSoftmaxWarps + 2) * 32;   // 0..63
-            const int width = kTrN + p.T - 1;
+            const int width = kTrN + p.T - 1 + 3;
             int n = 0, cut = 0, cut_b = 0, cut_g = 0;
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -583,8 +609,30 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     int* kpos = reinterpret_cast<int*>(vis + kMaxTree * 4);
                     float* tab = reinterpret_cast<float*>(kpos + kTrN);
                     const int j0 = s.jbase + t * kTrN;
-                    // The slice starts at the nearest key's distance from depth 0 (0 with tree keys).
-                    const int dlo = max(s.ctx - j0 - (kTrN - 1), 0);
+                    // The slice starts at the nearest key's distance from depth 0 (0 with tree keys),
+                    // rounded down to a 16-byte boundary.  Where the table ends in it, zeros follow.
+                    const int dlo = max(s.ctx - j0 - (kTrN - 1), 0) & ~3;
+                    const int in = min(max(p.R - dlo, 0), (width + 3) & ~3);
+                    const float* src = p.w + static_cast<size_t>(s.g) * p.G * p.R + dlo;
+                    if (p.w_bulk) {
+                        // Every row starts on a 16-byte boundary and `in` is a multiple of 4.
+                        if (warp == kTrSoftmaxWarps + 2) {
+                            if (lane == 0 && in > 0) mbar_expect_tx(&sh->tab_full[buf], p.G * in * 4);
+                            __syncwarp();
+                            if (in > 0 && lane < p.G)
+                                bulk_load(tab + lane * tstride, src + static_cast<size_t>(lane) * p.R, in * 4,
+                                          &sh->tab_full[buf]);
+                        }
+                    } else {
+                        for (int h = 0; h < p.G; ++h)
+                            for (int x = x0; x < min(in, width); x += 64)
+                                cp_async4(tab + h * tstride + x, src + static_cast<size_t>(h) * p.R + x);
+                    }
+                    if (in < width) {
+                        for (int h = 0; h < p.G; ++h)
+                            for (int x = in + x0; x < width; x += 64) tab[h * tstride + x] = 0.0f;
+                        fence_proxy_async_shared();   // before later bulk copies into the same place
+                    }
                     if (j0 + kTrN > s.ctx) {
                         // Position of each key less ctx; dead keys are in no mask.
                         for (int c = x0; c < kTrN; c += 64) {
@@ -605,15 +653,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             vis[x] = __funnelshift_r(word(bit >> 5), word((bit >> 5) + 1), bit & 31);
                         }
                     }
-                    const float* src = p.w + static_cast<size_t>(s.g) * p.G * p.R + dlo;
-                    for (int h = 0; h < p.G; ++h, src += p.R)
-                        for (int x = x0; x < width; x += 64) {
-                            if (dlo + x < p.R)
-                                cp_async4(tab + h * tstride + x, src + x);
-                            else
-                                tab[h * tstride + x] = 0.0f;
-                        }
-                    cp_async_wait_all();
+                    if (!p.w_bulk) cp_async_wait_all();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->tab_full[buf]);
                 }
@@ -681,7 +721,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (slice && !(ok = tree_all(mbar_wait(&sh->tab_full[buf], use & 1, abort_flag)))) break;
                 tc_fence_after();
                 const int own0 = ctx - j0 - half * 64;         // this half's first column with a tree key
-                const int dlo = max(ctx - j0 - (kTrN - 1), 0);   // the slice's first distance
+                const int dlo = max(ctx - j0 - (kTrN - 1), 0) & ~3;   // the slice's first distance
                 if (own0 < 64) {
                     // Bias and masks of the chunks with tree keys, back into S.
                     const uint32_t* mine_vis = vis + (row_ok ? (t_node - 2 * grp * npt) * 4 : 0) + half * 2;
@@ -700,7 +740,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             for (int f = 0; f < 4; ++f) {
                                 const int dist = dep - ks[f];
                                 if (static_cast<unsigned>(dist) >= static_cast<unsigned>(wlim)) see &= ~(1u << (4 * e + f));
-                                w[4 * e + f] = tab[min(max(dist - dlo, 0), kTrN - 1 + p.T - 1)];
+                                w[4 * e + f] = tab[min(max(dist - dlo, 0), kTrN + p.T + 1)];
                             }
                         }
                         tmem_ld_wait_regs16(sr);
@@ -866,7 +906,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 a_other *= inv;
             }
             const int h = s.g * p.G + hh;
-            const size_t orow = (static_cast<size_t>(s.b) * p.T + t_node) * p.Hq + h;
+            // Output rows: of the sequence's first node and head 0, and this thread's from there.
+            const size_t obase = static_cast<size_t>(s.b) * p.T * p.Hq;
+            const int orow = t_node * p.Hq + h;
+            const unsigned ok_rows = __ballot_sync(0xffffffffu, row_ok);
             // A run's first cut segment goes to its partial 0 if it comes from the run before, else to 1.
             float* rec = p.part + (static_cast<size_t>(blockIdx.x * 2 + (left ? 0 : 1)) * p.part_rows +
                                    (two ? ls * kTrM : 0) + ri) * (D + kTrRec);
@@ -888,19 +931,41 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     v[e] = own ? __uint_as_float(y[e]) * a_own : 0.0f;
                     v[e] = other ? fmaf(__uint_as_float(z[e]), a_other, v[e]) : v[e];
                 }
-                if (row_ok) {
-                    if (direct) {
+                // A thread holds 32 columns of its row; groups of four lanes trade 16-byte pieces, so
+                // that a store writes 64 bytes of each of eight rows and not 16 of 32 (the lines that a
+                // store touches are its cost: 3.5k -> 1.3k cycles per segment).
+                if (direct) {
+                    uint4 u[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            if (e < cols)
-                                st_global_v4(p.o + orow * D + c + e, pack_bf16x2(v[e], v[e + 1]),
-                                             pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]),
-                                             pack_bf16x2(v[e + 6], v[e + 7]));
-                    } else {
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                          pack_bf16x2(v[8 * e + 4], v[8 * e + 5]),
+                                          pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+                    tree_transpose4(u, lane);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            if (e < cols)
-                                *reinterpret_cast<float4*>(rec + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const int from = (lane & ~3) + e, at = __shfl_sync(0xffffffffu, orow, from);
+                        if (((ok_rows >> from) & 1u) && (lane & 3) * 8 < cols)
+                            st_global_v4(p.o + (obase + at) * D + c + (lane & 3) * 8, u[e].x, u[e].y, u[e].z, u[e].w);
+                    }
+                } else {
+#pragma unroll
+                    for (int x2 = 0; x2 < 2; ++x2) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float* f = v + 16 * x2 + 4 * e;
+                            u[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                              __float_as_uint(f[3]));
+                        }
+                        tree_transpose4(u, lane);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int from = (lane & ~3) + e;
+                            if (((ok_rows >> from) & 1u) && 16 * x2 < cols)
+                                *reinterpret_cast<uint4*>(rec + (from - lane) * (D + kTrRec) + c + 16 * x2 +
+                                                          (lane & 3) * 4) = u[e];
+                        }
                     }
                 }
             }
