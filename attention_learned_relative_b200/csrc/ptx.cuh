@@ -370,6 +370,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ---------------------------------------------------------------- misc
+// In a kernel launched with programmatic serialisation: waits until the kernel before it in
+// the stream has finished and its writes are visible.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -74,7 +74,6 @@ constexpr int kTrMinTiles = 1;             // least key tiles of a CTA's run
 constexpr int kTrRec = 4;                  // floats of a partial record beyond its output: max, sum, pad
 constexpr int kTrMaxStages = 4;            // of K, and of V
 constexpr int kTrLongSegment = 32;         // key tiles of a segment that counts as long
-constexpr int kTrEmuPer8 = 0;              // of eight pairs of exponentials, those taken on the FMA pipe
 constexpr int kTrSegs = 4;                 // published segments
 
 template <int D>
@@ -116,31 +115,6 @@ constexpr int kTrSharedBytes = (static_cast<int>(sizeof(TreeShared)) + 15) / 16 
 // slice starts on a 16-byte boundary of its table row), in a stride that is 4 modulo 32, so
 // that eight heads at one depth meet eight different banks.
 __host__ __device__ constexpr int tree_tab_stride(int T) { return (kTrN + T - 1 + 31) / 32 * 32 + 4; }
-
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number (the sum with
-// 1.5 * 2^23 has it in its low bits) and |f| <= 1/2, 2^f by its Taylor polynomial of degree 6
-// in f ln 2 (the first term left out is below 1.3e-7 of 2^f, an ulp of fp32), n added to the
-// exponent.  x is at most a few units above 0; below -126 the result is 2^-126, which no
-// sum or bf16 weight next to the row's largest can see, so a masked key (x = -inf) is set
-// to 0 apart.
-__device__ __forceinline__ uint64_t tree_exp2(uint64_t x2) {
-    constexpr float kC[7] = {1.0f, 0.69314718f, 0.24022651f, 0.055504109f, 0.0096181291f, 0.0013333558f, 0.00015403530f};
-    float a, b;
-    f2_unpack(x2, a, b);
-    const uint64_t x = f2_pack(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
-    const uint64_t y = f2_add(x, f2_pack(12582912.0f, 12582912.0f));
-    const uint64_t n = f2_add(y, f2_pack(-12582912.0f, -12582912.0f));
-    const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
-    uint64_t q = f2_pack(kC[6], kC[6]);
-#pragma unroll
-    for (int i = 5; i >= 0; --i) q = f2_fma(q, f, f2_pack(kC[i], kC[i]));
-    float qa, qb, ya, yb;
-    f2_unpack(q, qa, qb);
-    f2_unpack(y, ya, yb);
-    qa = __uint_as_float(__float_as_uint(qa) + (__float_as_uint(ya) << 23));
-    qb = __uint_as_float(__float_as_uint(qb) + (__float_as_uint(yb) << 23));
-    return f2_pack(a == -INFINITY ? 0.0f : qa, b == -INFINITY ? 0.0f : qb);
-}
 
 // A buffer of the stagers: masks of up to 128 nodes, four words each; key positions; a slice
 // per head.
@@ -589,7 +563,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // ------------------------------------------------------------ stagers
             const int x0 = threadIdx.x - (kTrSoftmaxWarps + 2) * 32;   // 0..63
             const int width = kTrN + p.T - 1 + 3;
-            int n = 0, cut = 0, cut_b = 0, cut_g = 0;
+            int n = 0;
+            int4 cut = make_int4(0, 0, 0, 0);
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 if (!(ok = seg_wait(i))) break;
@@ -599,8 +574,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const int after = s.nt - s.tile0 - s.ntiles;
                 if (s.tile0 == 0 && after > 0) {
                     // The segment starts here and goes on in the next runs.
-                    cut = 1 + (after + s.per - 1) / s.per;
-                    cut_b = s.b, cut_g = s.g;
+                    cut = make_int4(1 + (after + s.per - 1) / s.per, s.b, s.g, s.n);
                 }
                 for (int t = s.first_slice; t < s.ntiles; ++t, ++n) {
                     const int buf = p.tab_bufs == 2 ? n & 1 : 0, use = p.tab_bufs == 2 ? n >> 1 : n;
@@ -658,7 +632,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (lane == 0) mbar_arrive(&sh->tab_full[buf]);
                 }
             }
-            if (x0 == 0) p.cuts[blockIdx.x] = make_int4(cut, cut_b, cut_g, 0);
+            if (x0 == 0) p.cuts[blockIdx.x] = cut;
         }
     } else {
         // ---------------------------------------------------------------- softmax / epilogue
@@ -691,7 +665,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const TreeSeg& s = sh->segs[i % kTrSegs];
             const int ntiles = s.ntiles;
             if (ntiles == 0) break;
-            const int two = s.two, ctx = s.ctx, first_slice = s.first_slice, jbase = s.jbase;
+            const int two = s.two, ctx = s.ctx, nodes = s.n, first_slice = s.first_slice, jbase = s.jbase;
             const int ls = slot ^ parity;      // this slot's part: its row tile, or its half of the key tiles
             const int t_node = row.t;
             const bool row_ok = row.ok;
@@ -727,6 +701,15 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     const uint32_t* mine_vis = vis + (row_ok ? (t_node - 2 * grp * npt) * 4 : 0) + half * 2;
 #pragma unroll 1
                     for (int cc = max(own0, 0) & ~15; cc < 64; cc += 16) {
+                        if (cc >= own0 + nodes) {   // past the tree: nothing to look up
+                            uint32_t none[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) none[e] = 0xff800000u;
+                            tmem_st16(s_tm + cc, none);
+                            tmem_st_wait();
+                            tmem_regs_keep16(none);
+                            continue;
+                        }
                         uint32_t see = mine_vis[cc >> 5] >> (cc & 16);
                         uint32_t sr[16];
                         tmem_ld16(s_tm + cc, sr);
@@ -830,17 +813,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     tmem_ld_wait_regs(x);
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const uint64_t x2 =
-                            f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), c1x2, nm2);
                         float p0, p1;
-                        if (((c >> 1) & 7) < kTrEmuPer8) {
-                            f2_unpack(tree_exp2(x2), p0, p1);
-                        } else {
-                            float x0, x1;
-                            f2_unpack(x2, x0, x1);
-                            p0 = ex2_approx(x0);
-                            p1 = ex2_approx(x1);
-                        }
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), c1x2, nm2), p0, p1);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
                         acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
                         // Weights are rounded to bf16 for the tensor cores (2^-8 of each at most,
                         // while their sum stays in fp32).
@@ -993,36 +969,64 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 }
 
 // Merges the partials of the segment that starts in run blockIdx.y and goes on in later
-// runs (at most one per run): one warp per row.
-constexpr int kTrCombineWarps = 8;
+// runs (at most one per run): one warp per row.  Bounded by three dependent loads (the cut,
+// the maxima and sums, the outputs); those of the first parts are issued together.
+constexpr int kTrCombineWarps = 4, kTrCombineAhead = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(const TreeAttnParams p) {
     constexpr int E = D / 32;
-    const int4 cut = p.cuts[blockIdx.y];   // {parts, sequence, key/value head, -}
+    grid_dependency_wait();
+    const int4 cut = p.cuts[blockIdx.y];   // {parts, sequence, key/value head, nodes}
     if (cut.x == 0) return;
     const int lane = threadIdx.x & 31, ri = blockIdx.x * kTrCombineWarps + (threadIdx.x >> 5);
     const int grp = blockIdx.y % p.groups, npt = kTrM / p.G;
     const int node = (ri & (kTrM - 1)) / p.G, hh = (ri & (kTrM - 1)) - node * p.G;
     const int t = (2 * grp + ri / kTrM) * npt + node, h = cut.z * p.G + hh;
-    const TreeSeq q = tree_seq(p, __ldg(p.ctx_lens + cut.y), __ldg(p.tree_lens + cut.y));
-    if (node >= npt || t >= q.n) return;
+    if (node >= npt || t >= cut.w) return;
     // Part 0 is partial 1 of its run, the others partial 0 of theirs.
     auto rec = [&](int s) {
         return p.part + (static_cast<size_t>((blockIdx.y + s * p.groups) * 2 + (s == 0 ? 1 : 0)) * p.part_rows + ri) *
                             (D + kTrRec);
     };
-    float M = -INFINITY;
-    for (int s = lane; s < cut.x; s += 32) M = fmaxf(M, rec(s)[D]);
+    float2 ahead[kTrCombineAhead][E / 2];
+#pragma unroll
+    for (int s = 0; s < kTrCombineAhead; ++s)
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            ahead[s][e / 2] = s < cut.x ? *reinterpret_cast<const float2*>(rec(s) + lane * E + e) : make_float2(0.f, 0.f);
+    // Lane x holds the max and sum of parts x, x + 32, ... merged.
+    float m = -INFINITY, l = 0.0f, m_own = -INFINITY;
+    for (int s = lane; s < cut.x; s += 32) {
+        const float2 ml = *reinterpret_cast<const float2*>(rec(s) + D);
+        const float top = fmaxf(m, ml.x);
+        const float a = m == -INFINITY ? 0.0f : ex2_approx(m - top);
+        l = l * a + (ml.x == -INFINITY ? 0.0f : ml.y * ex2_approx(ml.x - top));
+        m = top;
+        if (s == lane) m_own = ml.x;
+    }
+    float M = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float l = 0.0f, acc[E] = {};
+    l = m == -INFINITY ? 0.0f : l * ex2_approx(m - M);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float w_own = m_own == -INFINITY ? 0.0f : ex2_approx(m_own - M);
+    float acc[E] = {};
+#pragma unroll
+    for (int s = 0; s < kTrCombineAhead; ++s) {
+        const float a = __shfl_sync(0xffffffffu, w_own, s);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            acc[e] = fmaf(ahead[s][e / 2].x, a, acc[e]);
+            acc[e + 1] = fmaf(ahead[s][e / 2].y, a, acc[e + 1]);
+        }
+    }
 #pragma unroll 4
-    for (int s = 0; s < cut.x; ++s) {
+    for (int s = kTrCombineAhead; s < cut.x; ++s) {
         const float* x = rec(s);
-        const float2 ml = *reinterpret_cast<const float2*>(x + D);
-        const float a = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-        l = fmaf(ml.y, a, l);
+        const float ms = x[D];
+        const float a = ms == -INFINITY ? 0.0f : ex2_approx(ms - M);
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
             const float2 v = *reinterpret_cast<const float2*>(x + lane * E + e);
@@ -1051,9 +1055,17 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     e = cudaGetLastError();
     if (e != cudaSuccess || p.max_tiles == 1) return e;   // a segment of one tile is never cut
     const int rows = p.part_rows > kTrM ? p.part_rows : p.T * p.G;
-    tree_combine_kernel<D><<<dim3((rows + kTrCombineWarps - 1) / kTrCombineWarps, ctas), kTrCombineWarps * 32, 0,
-                             stream>>>(p);
-    return cudaGetLastError();
+    // The combine is brought up while the kernel before it runs, and waits for it on the device.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((rows + kTrCombineWarps - 1) / kTrCombineWarps, ctas);
+    cfg.blockDim = dim3(kTrCombineWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p);
 }
 
 }  // namespace
