@@ -213,6 +213,7 @@ struct TreeAttnParams {
     int runs;                        // runs of a pair's tile stream
     int part_rows;                   // rows of a partial
     int max_tiles;                   // key tiles of the longest segment there may be
+    bool whole;                      // runs take the whole segments that start in them; none is cut
     int nq, nk, nv, tab_bufs;        // Q buffers, K and V stages, buffers of the stagers (set at the launch)
     int num_pages, page_size, max_pages, max_ctx;
     // x / page_size = x * page_mul >> page_shift for 0 <= x < 2^31
@@ -232,6 +233,7 @@ struct TreeLaunch {
     size_t cut_bytes, bytes;
 };
 int tree_max_tiles(int T, int max_ctx, int window, int box_rows);
+bool tree_whole_segments(int B, int Hkv, int runs, int max_tiles);
 TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int window, int d, int sms);
 // tq: 128 / G tokens by G heads per box (make_map's `heads`); tk, tv over the page pool,
 // box_rows rows per box.

@@ -279,6 +279,7 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.runs = plan.runs;
     p.part_rows = plan.part_rows;
     p.max_tiles = tree_max_tiles(T, max_ctx_len, p.window, p.box_rows);
+    p.whole = tree_whole_segments(B, Hkv, p.runs, p.max_tiles);
     p.cuts = static_cast<int4*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cut_bytes);
     CUtensorMap tq, tk, tv;

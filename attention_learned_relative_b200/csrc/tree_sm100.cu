@@ -22,7 +22,8 @@
 // an equal run of it: every CTA works for the same time whatever the lengths, in one wave.
 // A run covers the end of one segment, whole segments, and the start of another; whole
 // segments are written out directly, the two cut ones as partials (unnormalised output,
-// max, sum) that the combine kernel merges.  CTAs of different row pairs run the same
+// max, sum) that the combine kernel merges.  Where segments are short and many, a run takes
+// the whole segments that start in it instead: nothing is cut, and nothing combined.  CTAs of different row pairs run the same
 // stream side by side, so a K/V tile comes from HBM once and from L2 for the others.
 //
 // Warp roles (640 threads):
@@ -74,6 +75,7 @@ constexpr int kTrMinTiles = 1;             // least key tiles of a CTA's run
 constexpr int kTrRec = 4;                  // floats of a partial record beyond its output: max, sum, pad
 constexpr int kTrMaxStages = 4;            // of K, and of V
 constexpr int kTrLongSegment = 32;         // key tiles of a segment that counts as long
+constexpr int kTrCutTiles = 6;             // what cutting segments costs, in key tiles
 constexpr int kTrSegs = 4;                 // published segments
 
 template <int D>
@@ -216,7 +218,7 @@ struct TreeWalk {
                 prefix += __shfl_sync(0xffffffffu, scan, 31);
                 continue;
             }
-            const int w = __ffs(hit) - 1;
+            const int w = __ffs(hit) - 1;   // the sequence that holds the run's first tile
             b = x0 + w;
             const int rest = pos - prefix - __shfl_sync(0xffffffffu, scan - mine, w);
             q.ctx = __shfl_sync(0xffffffffu, s.ctx, w);
@@ -225,6 +227,11 @@ struct TreeWalk {
             q = tree_seq(p, q.ctx, q.n);
             g = rest / q.nt;
             off = rest - g * q.nt;
+            if (p.whole && off > 0) {   // its segment belongs to the run before
+                pos += q.nt - off;
+                off = 0;
+                ++g;
+            }
             return;
         }
     }
@@ -239,7 +246,7 @@ struct TreeWalk {
         }
         s.b = b, s.g = g, s.ctx = q.ctx, s.n = q.n, s.lo = q.lo, s.end = q.end, s.nt = q.nt;
         s.tile0 = off;
-        s.ntiles = min(q.nt - off, stop - pos);
+        s.ntiles = p.whole ? q.nt : min(q.nt - off, stop - pos);
         s.jbase = q.base + off * kTrN;
         s.two = (2 * grp + 1) * npt < q.n;
         // A tile has a slice if it holds a prefix key nearer than R to a node of depth 0, or a
@@ -572,7 +579,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 seg_done(i);
                 if (s.ntiles == 0) break;
                 const int after = s.nt - s.tile0 - s.ntiles;
-                if (s.tile0 == 0 && after > 0) {
+                if (s.tile0 == 0 && after > 0) {   // never, where runs take whole segments
                     // The segment starts here and goes on in the next runs.
                     cut = make_int4(1 + (after + s.per - 1) / s.per, s.b, s.g, s.n);
                 }
@@ -1053,7 +1060,7 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     const int ctas = p.runs * p.groups;
     tree_attn_kernel<D><<<ctas, kTrThreads, sm.bytes, stream>>>(tq, tk, tv, p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || p.max_tiles == 1) return e;   // a segment of one tile is never cut
+    if (e != cudaSuccess || p.whole) return e;   // nothing is cut
     const int rows = p.part_rows > kTrM ? p.part_rows : p.T * p.G;
     // The combine is brought up while the kernel before it runs, and waits for it on the device.
     cudaLaunchConfig_t cfg{};
@@ -1087,6 +1094,15 @@ TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int windo
     x.cut_bytes = (ctas * sizeof(int4) + 255) / 256 * 256;
     x.bytes = x.cut_bytes + ctas * 2 * x.part_rows * (d + kTrRec) * sizeof(float);
     return x;
+}
+
+// Whether runs take whole segments.  What cutting saves is the difference between the
+// longest run of whole segments and an even share of the tiles, at the most (segments of
+// the longest length); what it costs, partials and the combine kernel, is worth about
+// kTrCutTiles tiles (local layer of 64 sequences, 5-6 tiles a segment: WWW).
+bool tree_whole_segments(int B, int Hkv, int runs, int max_tiles) {
+    const long long items = static_cast<long long>(B) * Hkv;
+    return (items + runs - 1) / runs * max_tiles <= (items * max_tiles + runs - 1) / runs + kTrCutTiles;
 }
 
 cudaError_t launch_tree_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
