@@ -183,7 +183,7 @@ struct KvAppendParams {
     int num_slots;           // num_pages * page_size
     float eps;
 };
-cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, int d, cudaStream_t stream);
+cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, int d, int sms, cudaStream_t stream);
 
 struct KvCompactParams {
     void *k_pages, *v_pages; // [layers, num_pages, page_size, row_vecs] 16-byte vectors

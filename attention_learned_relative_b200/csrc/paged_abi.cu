@@ -134,7 +134,9 @@ extern "C" int relbias_kv_append(const void* q, const void* k, const void* v, co
     p.Hkv = Hkv;
     p.num_slots = num_pages * page_size;
     p.eps = eps;
-    const cudaError_t e = launch_kv_append(p, dtype == RELBIAS_BF16, d, static_cast<cudaStream_t>(stream));
+    DeviceInfo dev;
+    if ((rc = device_info(dev)) != RELBIAS_OK) return rc;
+    const cudaError_t e = launch_kv_append(p, dtype == RELBIAS_BF16, d, dev.sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RELBIAS_OK : cuda_fail(e, "cache write launch");
 }
 

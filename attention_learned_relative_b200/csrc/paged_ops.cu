@@ -272,76 +272,84 @@ struct Vec<__nv_bfloat16> {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const KvAppendParams p) {
     constexpr int N = Vec<T>::N;
     constexpr int kVecs = D / N;                       // 16-byte vectors of a head row
     constexpr int LANES = kVecs < 32 ? kVecs : 32;     // threads of a head row
     constexpr int VPL = kVecs / LANES;                 // vectors of a thread
     constexpr int kRows = kAppendThreads / LANES;      // rows of a block and pass
+    constexpr int kFlight = VPL == 1 ? kAppendRows : 2;
     const int sub = threadIdx.x % LANES;
     const unsigned heads = static_cast<unsigned>(p.heads_q + 2 * p.Hkv);
     const unsigned rows = static_cast<unsigned>(p.ntok) * heads;
-    const unsigned r0 = blockIdx.x * static_cast<unsigned>(kRows * kAppendRows) + threadIdx.x / LANES;
-
-    uint4 x[kAppendRows][VPL];
-    T* dst[kAppendRows];
-    const float* gain[kAppendRows];
+    // A thread's columns are the same in every row: their weights stay in registers.
+    float wq[VPL][N], wk[VPL][N];
 #pragma unroll
-    for (int u = 0; u < kAppendRows; ++u) {
-        const unsigned row = r0 + u * kRows;
-        dst[u] = nullptr;
-        gain[u] = nullptr;
+    for (int v = 0; v < VPL; ++v)
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) x[u][v] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= rows) continue;
-        const unsigned tok = row / heads;
-        int h = static_cast<int>(row - tok * heads);
-        const int slot = __ldg(p.slots + tok);
-        const T* src;
-        T* to;
-        if (h < p.heads_q) {
-            src = static_cast<const T*>(p.q) + static_cast<size_t>(tok) * p.q_stride + h * D;
-            to = static_cast<T*>(p.q_out) + (static_cast<size_t>(tok) * p.heads_q + h) * D;
-            gain[u] = p.q_weight;
-        } else {
-            h -= p.heads_q;
-            const bool is_v = h >= p.Hkv;
-            if (is_v) h -= p.Hkv;
-            src = static_cast<const T*>(is_v ? p.v : p.k) + static_cast<size_t>(tok) * (is_v ? p.v_stride : p.k_stride) +
-                  h * D;
-            to = static_cast<T*>(is_v ? p.v_pages : p.k_pages) + (static_cast<size_t>(max(slot, 0)) * p.Hkv + h) * D;
-            if (!is_v) gain[u] = p.k_weight;
+        for (int e = 0; e < N; ++e) {
+            const int c = (v * LANES + sub) * N + e;
+            wq[v][e] = p.q_weight != nullptr ? __ldg(p.q_weight + c) : 0.0f;
+            wk[v][e] = p.k_weight != nullptr ? __ldg(p.k_weight + c) : 0.0f;
+        }
+    for (unsigned r0 = blockIdx.x * static_cast<unsigned>(kRows * kFlight); r0 < rows;
+         r0 += gridDim.x * static_cast<unsigned>(kRows * kFlight)) {
+        uint4 x[kFlight][VPL];
+        T* dst[kFlight];
+        int kind[kFlight];   // 0: query, 1: key, 2: value
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const unsigned row = min(r0 + u * kRows + threadIdx.x / LANES, rows - 1);
+            const unsigned tok = row / heads;
+            int h = static_cast<int>(row - tok * heads);
+            const int slot = __ldg(p.slots + tok);
+            const T* src;
+            if (h < p.heads_q) {
+                src = static_cast<const T*>(p.q) + static_cast<size_t>(tok) * p.q_stride + h * D;
+                dst[u] = static_cast<T*>(p.q_out) + (static_cast<size_t>(tok) * p.heads_q + h) * D;
+                kind[u] = 0;
+            } else {
+                h -= p.heads_q;
+                kind[u] = h < p.Hkv ? 1 : 2;
+                if (kind[u] == 2) h -= p.Hkv;
+                src = static_cast<const T*>(kind[u] == 2 ? p.v : p.k) +
+                      static_cast<size_t>(tok) * (kind[u] == 2 ? p.v_stride : p.k_stride) + h * D;
+                dst[u] = static_cast<T*>(kind[u] == 2 ? p.v_pages : p.k_pages) +
+                         (static_cast<size_t>(max(slot, 0)) * p.Hkv + h) * D;
+            }
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) x[u][v] = __ldg(reinterpret_cast<const uint4*>(src) + v * LANES + sub);
+            // Rows without a slot are padding; a slot outside the pool is refused and reported.
+            if (slot >= p.num_slots) atomicOr(&g_status, kStatusBadLength);
+            if (slot < 0 || slot >= p.num_slots || r0 + u * kRows + threadIdx.x / LANES >= rows) dst[u] = nullptr;
         }
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) x[u][v] = __ldg(reinterpret_cast<const uint4*>(src) + v * LANES + sub);
-        // Rows without a slot are padding; a slot outside the pool is refused and reported.
-        if (slot >= 0 && slot < p.num_slots) dst[u] = to;
-        if (slot >= p.num_slots) atomicOr(&g_status, kStatusBadLength);
-    }
-#pragma unroll
-    for (int u = 0; u < kAppendRows; ++u) {
-        float f[VPL][N];
-        float ss = 0.0f;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            Vec<T>::unpack(x[u][v], f[v]);
-#pragma unroll
-            for (int e = 0; e < N; ++e) ss = fmaf(f[v][e], f[v][e], ss);
-        }
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (dst[u] == nullptr) continue;
-        if (gain[u] != nullptr) {
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+        for (int u = 0; u < kFlight; ++u) {
+            float f[VPL][N];
+            float ss = 0.0f;
 #pragma unroll
             for (int v = 0; v < VPL; ++v) {
+                Vec<T>::unpack(x[u][v], f[v]);
 #pragma unroll
-                for (int e = 0; e < N; ++e) f[v][e] *= inv * __ldg(gain[u] + (v * LANES + sub) * N + e);
-                x[u][v] = Vec<T>::pack(f[v]);
+                for (int e = 0; e < N; ++e) ss = fmaf(f[v][e], f[v][e], ss);
             }
-        }
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) reinterpret_cast<uint4*>(dst[u])[v * LANES + sub] = x[u][v];
+            for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (dst[u] == nullptr) continue;
+            if ((kind[u] == 0 && p.q_weight != nullptr) || (kind[u] == 1 && p.k_weight != nullptr)) {
+                const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) f[v][e] *= inv * (kind[u] == 0 ? wq[v][e] : wk[v][e]);
+                    x[u][v] = Vec<T>::pack(f[v]);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < VPL; ++v)
+                st_global_v4(reinterpret_cast<uint4*>(dst[u]) + v * LANES + sub, x[u][v].x, x[u][v].y, x[u][v].z,
+                             x[u][v].w);
+        }
     }
 }
 
@@ -405,20 +413,25 @@ __global__ void __launch_bounds__(128) kv_compact_kernel(const KvCompactParams p
     }
 }
 
-template <typename T>
-cudaError_t launch_append(const KvAppendParams& p, int d, cudaStream_t stream) {
+template <typename T, int D>
+cudaError_t launch_append(const KvAppendParams& p, int sms, cudaStream_t stream) {
+    constexpr int vecs = D / Vec<T>::N;
+    constexpr int per = kAppendThreads / (vecs < 32 ? vecs : 32) * (vecs <= 32 ? kAppendRows : 2);
     const long long rows = static_cast<long long>(p.ntok) * (p.heads_q + 2 * p.Hkv);
-    const int vecs = d / Vec<T>::N;
-    const int per = kAppendThreads / (vecs < 32 ? vecs : 32) * kAppendRows;
-    const unsigned grid = static_cast<unsigned>((rows + per - 1) / per);
+    const int grid = static_cast<int>(std::min<long long>((rows + per - 1) / per, 4LL * sms));
+    kv_append_kernel<T, D><<<grid, kAppendThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_append(const KvAppendParams& p, int d, int sms, cudaStream_t stream) {
     switch (d) {
-        case 32: kv_append_kernel<T, 32><<<grid, kAppendThreads, 0, stream>>>(p); break;
-        case 64: kv_append_kernel<T, 64><<<grid, kAppendThreads, 0, stream>>>(p); break;
-        case 128: kv_append_kernel<T, 128><<<grid, kAppendThreads, 0, stream>>>(p); break;
-        case 256: kv_append_kernel<T, 256><<<grid, kAppendThreads, 0, stream>>>(p); break;
+        case 32: return launch_append<T, 32>(p, sms, stream);
+        case 64: return launch_append<T, 64>(p, sms, stream);
+        case 128: return launch_append<T, 128>(p, sms, stream);
+        case 256: return launch_append<T, 256>(p, sms, stream);
         default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -434,8 +447,8 @@ cudaError_t launch_tree_plan(const TreePlanParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, int d, cudaStream_t stream) {
-    return bf16 ? launch_append<__nv_bfloat16>(p, d, stream) : launch_append<float>(p, d, stream);
+cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, int d, int sms, cudaStream_t stream) {
+    return bf16 ? launch_append<__nv_bfloat16>(p, d, sms, stream) : launch_append<float>(p, d, sms, stream);
 }
 
 cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream) {

@@ -585,14 +585,17 @@ def _token_stride(t, name: str, lead: tuple) -> int:
     shape, st = t.shape, t.stride()
     heads, d = shape[-2], shape[-1]
     ok = shape[:-2] == lead and (d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d)
-    step, span = None, 1
-    for i in range(len(lead) - 1, -1, -1):   # axes of one token have no say
-        if lead[i] > 1:
-            if step is None:
-                step = st[i]
-            elif st[i] != step * span:
-                ok = False
-        span *= lead[i]
+    if len(lead) == 1:
+        step = st[0] if lead[0] > 1 else None
+    else:
+        step, span = None, 1
+        for i in range(len(lead) - 1, -1, -1):   # axes of one token have no say
+            if lead[i] > 1:
+                if step is None:
+                    step = st[i]
+                elif st[i] != step * span:
+                    ok = False
+            span *= lead[i]
     if not ok:
         raise ValueError("%s must be [%s, heads, d] with dense heads and evenly spaced tokens" % (name, lead))
     return heads * d if step is None else step
