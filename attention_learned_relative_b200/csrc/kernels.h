@@ -180,6 +180,8 @@ struct KvAppendParams {
     void* q_out;             // [ntok, heads_q, d]
     void *k_pages, *v_pages; // [num_slots, Hkv, d]
     int ntok, heads_q, Hkv;  // heads_q = 0: no queries
+    uint64_t heads_mul;      // x / (heads_q + 2 Hkv) = x * heads_mul >> heads_shift for 0 <= x < 2^31
+    int heads_shift;
     int num_slots;           // num_pages * page_size
     float eps;
 };

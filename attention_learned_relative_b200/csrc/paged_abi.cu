@@ -20,6 +20,16 @@ int check_pool(int num_pages, int page_size, int max_pages) {
     return RELBIAS_OK;
 }
 
+// x / d = x * mul >> shift for 0 <= x < 2^31: with s = ceil(log2 d), mul = ceil(2^(31 + s) / d) is
+// above 2^(31 + s) / d by less than 1, so x * mul / 2^(31 + s) is above x / d by less than
+// 2^31 / 2^(31 + s) <= 1 / d and does not reach the next whole number.  mul < 2^33.
+void invariant_division(int d, uint64_t& mul, int& shift) {
+    int s = 0;
+    while ((1LL << s) < d) ++s;
+    shift = 31 + s;
+    mul = ((1ull << shift) + d - 1) / d;
+}
+
 template <typename... P>
 bool any_null(P... p) {
     return (... || (p == nullptr));
@@ -132,6 +142,7 @@ extern "C" int relbias_kv_append(const void* q, const void* k, const void* v, co
     p.ntok = ntok;
     p.heads_q = heads_q;
     p.Hkv = Hkv;
+    invariant_division(heads_q + 2 * Hkv, p.heads_mul, p.heads_shift);
     p.num_slots = num_pages * page_size;
     p.eps = eps;
     DeviceInfo dev;
@@ -263,13 +274,7 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     p.temp_n0 = temp_n0 > 1 ? temp_n0 : 0;
     p.inv_log_n0 = temp_n0 > 1 ? static_cast<float>(1.0 / std::log(static_cast<double>(temp_n0))) : 0.0f;
     p.box_rows = std::min(128, page_size & -page_size);
-    // Division by an invariant: with s = ceil(log2 page_size), m = ceil(2^(31 + s) / page_size)
-    // exceeds the quotient by less than 2^s / page_size units of 2^-(31 + s), which cannot reach
-    // the next whole number for x < 2^31.
-    int log2 = 0;
-    while ((1LL << log2) < page_size) ++log2;
-    p.page_shift = 31 + log2;
-    p.page_mul = ((1ull << p.page_shift) + page_size - 1) / page_size;
+    invariant_division(page_size, p.page_mul, p.page_shift);
     p.w_bulk = R % 4 == 0 && aligned16(w);
     if (static_cast<long long>(B) * Hkv * tree_max_tiles(T, max_ctx_len, p.window, 128) > INT32_MAX)
         return fail(RELBIAS_ERR_UNSUPPORTED, "too many key tiles (%d sequences, %d heads)", B, Hkv);

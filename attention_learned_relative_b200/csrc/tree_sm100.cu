@@ -23,8 +23,9 @@
 // A run covers the end of one segment, whole segments, and the start of another; whole
 // segments are written out directly, the two cut ones as partials (unnormalised output,
 // max, sum) that the combine kernel merges.  Where segments are short and many, a run takes
-// the whole segments that start in it instead: nothing is cut, and nothing combined.  CTAs of different row pairs run the same
-// stream side by side, so a K/V tile comes from HBM once and from L2 for the others.
+// the whole segments that start in it instead: nothing is cut, and nothing combined.  CTAs
+// of different row pairs run the same stream side by side, so a K/V tile comes from HBM
+// once and from L2 for the others.
 //
 // Warp roles (640 threads):
 //   warps 0-15      softmax and epilogue: slot = warp / 8, and within a slot two threads per
@@ -42,7 +43,10 @@
 // the run; the MMA warp issues QK(u), then PV(u - 1).  Products of one thread run in issue
 // order, so QK(u) may overwrite the P of unit u - 2, and when S(u) is complete O of its slot
 // holds all earlier units.  A slot's chain QK, softmax, PV, next QK sets the period of the
-// loop, not the products' rate, which is why a row's softmax is shared by two threads.
+// loop, not the products' rate, which is why a row's softmax is shared by two threads.  (One
+// thread per row, eight softmax warps with 128 columns in registers, was also built: 3%
+// faster on 131072-row caches with 64-node trees, 905-919 against 927-952 us, and 12% slower
+// on the local layer, 51.2 against 45.7 us, before runs of whole segments.)
 // Tensor memory: S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D); each half's P (bf16)
 // over the first half of its own columns of S.
 //
@@ -50,6 +54,7 @@
 // the bias on the way, and storing the sum back), and, once the row's two halves have met
 // and exchanged their maxima, for the weights.  The reference max of a row moves, and O is
 // rescaled, only when the max has grown by more than 2^8.
+//
 // Masks.  Sixteen-column chunks that hold tree keys are masked, and given their bias, by a
 // pass over S in tensor memory before the softmax reads it.  Other chunks add their bias in
 // registers, if any key is nearer than R, and are masked by one compare per key only in
@@ -640,6 +645,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 }
             }
             if (x0 == 0) p.cuts[blockIdx.x] = cut;
+            // Drain the bulk copies.  After an abort the second warp may be a slice behind the first,
+            // which issues them: it arrives in its place.
+            if (!ok && lane == 0 && warp == kTrSoftmaxWarps + 3)
+                for (int x = 0; x < p.tab_bufs; ++x) mbar_arrive(&sh->tab_full[x]);
+            if (p.w_bulk && warp == kTrSoftmaxWarps + 2)
+                for (int x = max(0, n - p.tab_bufs); x < n; ++x)
+                    mbar_drain_wait(&sh->tab_full[p.tab_bufs == 2 ? x & 1 : 0], (p.tab_bufs == 2 ? x >> 1 : x) & 1);
         }
     } else {
         // ---------------------------------------------------------------- softmax / epilogue
@@ -1099,7 +1111,7 @@ TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int windo
 // Whether runs take whole segments.  What cutting saves is the difference between the
 // longest run of whole segments and an even share of the tiles, at the most (segments of
 // the longest length); what it costs, partials and the combine kernel, is worth about
-// kTrCutTiles tiles (local layer of 64 sequences, 5-6 tiles a segment: WWW).
+// kTrCutTiles tiles (a local layer of 64 sequences, 5-6 tiles a segment: 45.8 us cut, 32.3 whole).
 bool tree_whole_segments(int B, int Hkv, int runs, int max_tiles) {
     const long long items = static_cast<long long>(B) * Hkv;
     return (items + runs - 1) / runs * max_tiles <= (items * max_tiles + runs - 1) / runs + kTrCutTiles;

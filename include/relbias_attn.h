@@ -465,10 +465,11 @@ RELBIAS_API int relbias_kv_append(const void* q, const void* k, const void* v, c
  * o = 0 and lse = -inf.  Cache rows that no node of a sequence sees by position (past its
  * tree, or before the window of its first node) may hold anything; the values of rows
  * inside that range must be finite, those of masked nodes included.
- * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; workspace of at
- * least relbias_attn_tree_paged_workspace_size(...) bytes, 16-byte aligned, whose
- * contents on entry do not matter.  Lengths out of range are clamped and page indices outside the pool
- * read zeros (RELBIAS_STATUS_BAD_LENGTH); a depth outside [0, T) is clamped
+ * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; max_ctx_len at
+ * most 2^30.  workspace: at least relbias_attn_tree_paged_workspace_size(...) bytes (for any
+ * page size), 16-byte aligned; its contents on entry do not matter, and calls that may overlap
+ * on the GPU need one each.  Lengths out of range are clamped and page indices outside the
+ * pool read zeros (RELBIAS_STATUS_BAD_LENGTH); a depth outside [0, T) is clamped
  * (RELBIAS_STATUS_BAD_TREE).
  */
 RELBIAS_API size_t relbias_attn_tree_paged_workspace_size(int B, int T, int Hq, int Hkv, int max_ctx_len, int d,

@@ -216,3 +216,111 @@ def test_workspace_and_another_stream():
     assert torch.equal(out, want)
     with pytest.raises(ops.RelbiasError):
         ops.attn_tree_paged(*args, scale=0.09, out=out, workspace=ws[:8])
+
+
+def _ragged(B, T, top, seed):
+    rng = np.random.default_rng(seed)
+    ctxs = rng.integers(0, top + 1, B)
+    lens = rng.integers(0, T + 1, B)
+    lens[rng.random(B) < 0.2] = 0
+    ctxs[rng.random(B) < 0.2] = 0
+    return [int(c) for c in ctxs], [int(n) for n in lens]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,page,window,bound", [
+    (70, 20, 16, 1, 64, 16, 0, 0),         # three row tiles a head: CTAs for two pairs of them
+    (70, 20, 16, 1, 64, 16, 0, 100000),    # segments are cut: the bound on the prefixes is far above them
+    (33, 5, 8, 2, 128, 32, 100, 0),
+    (100, 3, 8, 4, 64, 48, 0, 60000),
+    (40, 40, 16, 2, 128, 16, 50, 0),       # five row tiles: three pairs, the last of one
+    (40, 40, 16, 2, 128, 16, 0, 50000),
+])
+def test_large_ragged_batches(B, T, Hq, Hkv, d, page, window, bound):
+    """More sequences than a warp has lanes, some without a prefix, a tree, or rows of every
+    pair of row tiles; runs of whole and of cut segments."""
+    ctxs, lens = _ragged(B, T, 400, seed=B + T)
+    x = make(ctxs, lens, T, Hq, Hkv, d, page, window, 64, seed=B)
+    if bound:
+        x["table"] = torch.nn.functional.pad(x["table"], (0, bound // page), value=-7)
+    check(x, max_ctx=bound or None, what="ragged")
+
+
+@pytest.mark.parametrize("R", [1, 2, 3, 5, 127, 130, 301])
+def test_tables_that_bulk_copies_cannot_take(R):
+    """Tables whose rows do not start on 16-byte boundaries, by R or by their address."""
+    x = make([300, 77], [9, 16], 16, 8, 2, 128, 16, 0, R, seed=R)
+    check(x)
+    buf = torch.zeros(8 * R + 1, device="cuda")
+    buf[1:] = x["w"].view(-1)
+    x["w"] = buf[1:].view(8, R)
+    check(x)
+
+
+def test_a_table_that_starts_off_a_16_byte_boundary():
+    x = make([300, 77], [9, 16], 16, 8, 2, 128, 16, 0, 64, seed=3)
+    buf = torch.zeros(8 * 64 + 1, device="cuda")
+    buf[1:] = x["w"].view(-1)
+    x["w"] = buf[1:].view(8, 64)
+    check(x)
+
+
+def test_outputs_and_workspace_stay_in_bounds():
+    """Output, log-sum-exp and workspace sit between bands that must survive."""
+    x = make([900, 200, 3000], [16, 9, 3], 16, 16, 2, 128, 32, 0, 128, seed=7)
+    want, want_lse = call(x, 0.09)
+    size = ops.tree_workspace_size(3, 16, 16, 2, 3000, 128, 0)
+    band = 4096
+    raw = torch.full((size + 2 * band,), 171, dtype=torch.uint8, device="cuda")
+    o_raw = torch.full((want.numel() + 2 * band,), 9.0, dtype=torch.bfloat16, device="cuda")
+    l_raw = torch.full((want_lse.numel() + 2 * band,), 9.0, device="cuda")
+    out = o_raw[band:-band].view_as(want)
+    lse = l_raw[band:-band].view_as(want_lse)
+    ops.attn_tree_paged(x["q"], x["k_pages"], x["v_pages"], x["table"], _i32(x["ctxs"]), _i32(x["lens"]),
+                        _i32(x["depth"]), torch.as_tensor(mask_words(x["anc"])).cuda(), x["r"], x["w"], 0, 128, 3000,
+                        scale=0.09, out=out, lse=lse, workspace=raw[band:-band])
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert (raw[:band] == 171).all() and (raw[-band:] == 171).all()
+    assert (o_raw[:band] == 9).all() and (o_raw[-band:] == 9).all()
+    assert (l_raw[:band] == 9).all() and (l_raw[-band:] == 9).all()
+
+
+def test_two_streams_with_a_workspace_each():
+    x = make([2000, 700], [16, 9], 16, 16, 2, 128, 32, 0, 128, seed=17)
+    y = make([100, 1700], [5, 16], 16, 16, 2, 128, 32, 0, 128, seed=18)
+    want = [call(z, 0.09)[0] for z in (x, y)]
+    args = [(z["q"], z["k_pages"], z["v_pages"], z["table"], _i32(z["ctxs"]), _i32(z["lens"]), _i32(z["depth"]),
+             torch.as_tensor(mask_words(z["anc"])).cuda(), z["r"], z["w"], 0, 128, max(z["ctxs"])) for z in (x, y)]
+    outs = [torch.full_like(w, 9.0) for w in want]
+    size = ops.tree_workspace_size(2, 16, 16, 2, 2000, 128, 0)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for a, o, s, b in zip(args, outs, streams, ws):
+            ops.attn_tree_paged(*a, scale=0.09, out=o, workspace=b, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_waits_that_run_out_leave_the_next_call_clean():
+    """With a limit of a nanosecond ordinary waits give up: the call returns and reports it,
+    and the next one under the default limit is right."""
+    B, T, Hq, Hkv, d, page, ctx = 4, 16, 32, 4, 128, 256, 65536
+    x = make([8] * B, [T] * B, T, Hq, Hkv, d, page, 0, 64, seed=21)
+    blocks = ctx // page + 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for n in ("k_pages", "v_pages"):
+        x[n] = torch.randn(B * blocks, page, Hkv, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    x["table"] = torch.arange(B * blocks, dtype=torch.int32, device="cuda").view(B, blocks)
+    x["ctxs"] = [ctx] * B
+    want, _ = call(x, 0.09)
+    try:
+        ops.set_wait_limit_ns(1)
+        for _ in range(3):
+            call(x, 0.09)
+        assert ops.device_status(reset=True) & ops.RELBIAS_STATUS_TIMEOUT
+    finally:
+        ops.set_wait_limit_ns(0)
+    out, _ = call(x, 0.09)
+    assert ops.device_status(reset=True) == 0 and torch.equal(out, want)
