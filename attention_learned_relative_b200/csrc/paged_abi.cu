@@ -60,8 +60,13 @@ extern "C" int relbias_page_plan(const int* ctx_lens, const int* new_lens, const
     if (!all_aligned4(ctx_lens, new_lens, num_blocks, num_blocks_out, block_table, free_ring, ring_state,
                       ring_state_out, granted, slots))
         return fail(RELBIAS_ERR_ARG, "all arrays must be 4-byte aligned");
-    if (ring_state == ring_state_out || (B > 0 && num_blocks == num_blocks_out))
-        return fail(RELBIAS_ERR_ARG, "ring_state_out and num_blocks_out must not be the arrays they update");
+    // Every block reads the inputs of all requests before its own: no output may be one of them.
+    for (const void* out : {static_cast<const void*>(ring_state_out), static_cast<const void*>(num_blocks_out),
+                            static_cast<const void*>(granted), static_cast<const void*>(slots)})
+        for (const void* in : {static_cast<const void*>(ring_state), static_cast<const void*>(num_blocks),
+                               static_cast<const void*>(ctx_lens), static_cast<const void*>(new_lens)})
+            if (out != nullptr && out == in)
+                return fail(RELBIAS_ERR_ARG, "num_blocks_out, ring_state_out, granted and slots must not be inputs");
     PagePlanParams p{};
     p.ctx_lens = ctx_lens;
     p.new_lens = new_lens;
@@ -232,6 +237,7 @@ extern "C" int relbias_attn_tree_paged(const void* q, const void* k_pages, const
     if (max_ctx_len < 0 || static_cast<long long>(max_ctx_len) > static_cast<long long>(max_pages) * page_size)
         return fail(RELBIAS_ERR_ARG, "max_ctx_len (%d) must be in [0, max_pages * page_size]", max_ctx_len);
     if (dtype != RELBIAS_BF16) return fail(RELBIAS_ERR_UNSUPPORTED, "the tree attention is bf16 only");
+    if (R > 1 << 30) return fail(RELBIAS_ERR_UNSUPPORTED, "R (%d) is past 2^30", R);
     if ((rc = check_tree_shape(B, T, Hq, Hkv, max_ctx_len, d)) != RELBIAS_OK) return rc;
     if (B == 0 || T == 0) return RELBIAS_OK;
     if (any_null(q, k_pages, v_pages, static_cast<const void*>(o), static_cast<const void*>(workspace)) ||

@@ -43,7 +43,10 @@
 // the run; the MMA warp issues QK(u), then PV(u - 1).  Products of one thread run in issue
 // order, so QK(u) may overwrite the P of unit u - 2, and when S(u) is complete O of its slot
 // holds all earlier units.  A slot's chain QK, softmax, PV, next QK sets the period of the
-// loop, not the products' rate, which is why a row's softmax is shared by two threads.  (One
+// loop, not the products' rate, which is why a row's softmax is shared by two threads, and
+// why one warp issues all products: with a warp for QK and one for PV the order of the two
+// has to go through a barrier, which costs the chain more than the warps gain (131072-row
+// case 1020 us against 870-918).  (One
 // thread per row, eight softmax warps with 128 columns in registers, was also built: 3%
 // faster on 131072-row caches with 64-node trees, 905-919 against 927-952 us, and 12% slower
 // on the local layer, 51.2 against 45.7 us, before runs of whole segments.)
@@ -1091,8 +1094,8 @@ cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 
 // Key tiles of the longest sequence: a windowed one may start up to a box before its first key.
 int tree_max_tiles(int T, int max_ctx, int window, int box_rows) {
-    const int rows = (window > 0 ? std::min(max_ctx, window - 1 + box_rows - 1) : max_ctx) + T;
-    return (rows + kTrN - 1) / kTrN;
+    const long long prefix = window > 0 ? std::min<long long>(max_ctx, window - 2LL + box_rows) : max_ctx;
+    return static_cast<int>((prefix + T + kTrN - 1) / kTrN);
 }
 
 TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int window, int d, int sms) {

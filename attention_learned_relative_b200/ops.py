@@ -9,6 +9,7 @@ raise, they never compute anything on the CPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -478,7 +479,8 @@ def attn_bwd_bank(q, k, v, rs, proj, o, lse, dout, window: int, R: int, scale: f
 
 
 # These calls take a few microseconds on the device, so their checks are kept short: one
-# comparison per tensor, no copies, and only tensors that the caller gave are looked at.
+# comparison per tensor, no copies, and only tensors that the caller gave are looked at.  Each
+# also takes `stream`, the stream to run on (default: the current one of the tensors' device).
 
 
 def _dense(t, name: str, dev: int, dtype, shape):
@@ -503,15 +505,30 @@ def _on(dev: int, fn, *args):
         return fn(*args)
 
 
-def _call(fn, dev: int, stream, *args):
-    """fn(*args, stream) with device `dev` current, on `stream` or that device's current stream."""
-    rc = _on(dev, fn, *args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+def _call(fn, dev: int, *args):
+    """fn(*args, stream) with device `dev` current, on that device's current stream."""
+    rc = _on(dev, fn, *args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != RELBIAS_OK:
         _check(rc)
 
 
+def _on_stream(fn):
+    """A `stream` argument: the call, and what it allocates, belongs to that stream."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        first = args[0] if args else next(iter(kw.values()))
+        if first.get_device() != stream.device.index:
+            raise ValueError("the stream is not on the tensors' device")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+@_on_stream
 def page_plan(ctx_lens, new_lens, num_blocks, block_table, free_ring, ring_state, page_size: int, T: int, slots=None,
-              granted=None, num_blocks_out=None, ring_state_out=None, stream=None):
+              granted=None, num_blocks_out=None, ring_state_out=None):
     """Block tables and slot maps of a step, built on the GPU from request lengths.
     ctx_lens, new_lens, num_blocks [B] int32: rows in the cache, rows to add (at most T)
     and pages held; block_table [B,max_pages] and free_ring [num_pages] int32, updated in
@@ -549,13 +566,14 @@ def page_plan(ctx_lens, new_lens, num_blocks, block_table, free_ring, ring_state
         ring_state_out = torch.empty_like(ring_state)
     else:
         _dense(ring_state_out, "ring_state_out", dev, i32, (2,))
-    _call(lib().relbias_page_plan, dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), num_blocks.data_ptr(),
+    _call(lib().relbias_page_plan, dev, ctx_lens.data_ptr(), new_lens.data_ptr(), num_blocks.data_ptr(),
           num_blocks_out.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(), ring_state.data_ptr(),
           ring_state_out.data_ptr(), granted.data_ptr(), slots.data_ptr(), B, T, int(page_size), max_pages, num_pages)
     return slots, granted, num_blocks_out, ring_state_out
 
 
-def tree_plan(parents, tree_lens, depth=None, mask=None, stream=None):
+@_on_stream
+def tree_plan(parents, tree_lens, depth=None, mask=None):
     """Positions and ancestor masks of drafted trees.  parents [B,T] int32 (the parent of
     each node, which comes before it; -1: a root), tree_lens [B] int32; T <= 128.  Returns
     (depth [B,T], mask [B,T,ceil(T/32)]) int32: bit s of node t's words is set if s is t or
@@ -574,7 +592,7 @@ def tree_plan(parents, tree_lens, depth=None, mask=None, stream=None):
         mask = parents.new_empty((B, T, words))
     else:
         _dense(mask, "mask", dev, i32, (B, T, words))
-    _call(lib().relbias_tree_plan, dev, stream, parents.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(),
+    _call(lib().relbias_tree_plan, dev, parents.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(),
           mask.data_ptr(), B, T)
     return depth, mask
 
@@ -601,8 +619,8 @@ def _token_stride(t, name: str, lead: tuple) -> int:
     return heads * d if step is None else step
 
 
-def kv_append(k, v, slots, k_pages, v_pages, q=None, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None,
-              stream=None):
+@_on_stream
+def kv_append(k, v, slots, k_pages, v_pages, q=None, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None):
     """New rows of a layer into its pages, with the per-head norm of queries and keys.
     k, v [...,Hkv,d] and q [...,Hq,d] (bf16 or fp32; tokens may be strided, as slices of one
     projection's output are), slots [...] int32 with the cache row of each token (< 0:
@@ -637,7 +655,7 @@ def kv_append(k, v, slots, k_pages, v_pages, q=None, q_weight=None, k_weight=Non
         else:
             _dense(q_out, "q_out", dev, dtype, q.shape)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-    _call(lib().relbias_kv_append, dev, stream, q_ptr, k.data_ptr(), v.data_ptr(), slots.data_ptr(), qw_ptr,
+    _call(lib().relbias_kv_append, dev, q_ptr, k.data_ptr(), v.data_ptr(), slots.data_ptr(), qw_ptr,
           None if k_weight is None else k_weight.data_ptr(), out_ptr, k_pages.data_ptr(), v_pages.data_ptr(),
           lead.numel(), Hq, Hkv, d, q_stride, _token_stride(k, "k", lead), _token_stride(v, "v", lead), num_pages,
           page_size, float(eps), _dtype_code(k))
@@ -649,8 +667,9 @@ def tree_workspace_size(B: int, T: int, Hq: int, Hkv: int, max_ctx_len: int, d: 
     return int(lib().relbias_attn_tree_paged_workspace_size(B, T, Hq, Hkv, int(max_ctx_len), d, int(window)))
 
 
+@_on_stream
 def attn_tree_paged(q, k_pages, v_pages, block_table, ctx_lens, tree_lens, depth, mask, r, w, window: int, R: int,
-                    max_ctx_len: int, scale: float | None = None, out=None, lse=None, workspace=None, stream=None,
+                    max_ctx_len: int, scale: float | None = None, out=None, lse=None, workspace=None,
                     temp_n0: int = 0):
     """Attention of drafted trees over a paged cache.  q [B,T,Hq,d] bf16 (sequence b's tree is
     its first tree_lens[b] rows, whose keys and values are cache rows ctx_lens[b] + t),
@@ -692,7 +711,7 @@ def attn_tree_paged(q, k_pages, v_pages, block_table, ctx_lens, tree_lens, depth
     else:
         _need(workspace.get_device() == dev and workspace.is_contiguous(), "workspace must be dense, on q's device")
         ws_bytes = workspace.numel() * workspace.element_size()
-    _call(lib().relbias_attn_tree_paged, dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+    _call(lib().relbias_attn_tree_paged, dev, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           block_table.data_ptr(), ctx_lens.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(), mask.data_ptr(),
           r.data_ptr(), None if w is None else w.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
           B, T, num_pages, page_size, max_pages, max_ctx_len, Hq, Hkv, d, window, int(R),
@@ -701,7 +720,8 @@ def attn_tree_paged(q, k_pages, v_pages, block_table, ctx_lens, tree_lens, depth
     return out
 
 
-def kv_compact(k_pages, v_pages, block_table, ctx_lens, path, path_lens, stream=None):
+@_on_stream
+def kv_compact(k_pages, v_pages, block_table, ctx_lens, path, path_lens):
     """The accepted path's cache rows to the rows they keep, in place: row ctx_lens[b] + i
     receives row ctx_lens[b] + path[b,i] for i < path_lens[b].  k_pages/v_pages
     [num_pages,page_size,Hkv,d], or [layers,num_pages,page_size,Hkv,d] for all layers in one
@@ -719,7 +739,7 @@ def kv_compact(k_pages, v_pages, block_table, ctx_lens, path, path_lens, stream=
     _dense(ctx_lens, "ctx_lens", dev, i32, (B,))
     _dense(path, "path", dev, i32, (B, A))
     _dense(path_lens, "path_lens", dev, i32, (B,))
-    _call(lib().relbias_kv_compact, dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+    _call(lib().relbias_kv_compact, dev, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
           ctx_lens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), pool[0] if len(pool) == 5 else 1, B, A,
           num_pages, page_size, max_pages, Hkv, d, _dtype_code(k_pages))
 

@@ -399,7 +399,8 @@ RELBIAS_API int relbias_attn_bwd_bank(const void* q, const void* k, const void* 
  * earlier requests of the batch (refused ones included) are within `count`.  A refused
  * request keeps its pages and its row.  A request with a length or page count out of
  * range (or too long for max_pages) is refused and sets RELBIAS_STATUS_BAD_LENGTH, as does a
- * ring state that cannot be.  All arrays are device memory; one launch.
+ * ring state that cannot be.  All arrays are device memory; the outputs are not inputs; one
+ * launch.
  * num_pages * page_size and max_pages * page_size < 2^31.
  */
 RELBIAS_API int relbias_page_plan(const int* ctx_lens, const int* new_lens,
@@ -465,8 +466,8 @@ RELBIAS_API int relbias_kv_append(const void* q, const void* k, const void* v, c
  * o = 0 and lse = -inf.  Cache rows that no node of a sequence sees by position (past its
  * tree, or before the window of its first node) may hold anything; the values of rows
  * inside that range must be finite, those of masked nodes included.
- * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; max_ctx_len at
- * most 2^30.  workspace: at least relbias_attn_tree_paged_workspace_size(...) bytes (for any
+ * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; max_ctx_len and
+ * R at most 2^30.  workspace: at least relbias_attn_tree_paged_workspace_size(...) bytes (for any
  * page size), 16-byte aligned; its contents on entry do not matter, and calls that may overlap
  * on the GPU need one each.  Lengths out of range are clamped and page indices outside the
  * pool read zeros (RELBIAS_STATUS_BAD_LENGTH); a depth outside [0, T) is clamped

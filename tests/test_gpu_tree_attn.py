@@ -245,6 +245,18 @@ def test_large_ragged_batches(B, T, Hq, Hkv, d, page, window, bound):
     check(x, max_ctx=bound or None, what="ragged")
 
 
+def test_no_sequence_has_a_node():
+    x = make([30, 0, 5000], [0, 0, 0], 8, 8, 2, 64, 16, 0, 16, seed=1)
+    check(x)
+
+
+def test_a_window_of_any_size():
+    x = make([700, 40], [9, 16], 16, 8, 2, 128, 16, 0, 64, seed=5)
+    want, _ = call(x, 0.09)
+    x["window"] = 2 ** 31 - 1
+    assert torch.equal(call(x, 0.09)[0], want)
+
+
 @pytest.mark.parametrize("R", [1, 2, 3, 5, 127, 130, 301])
 def test_tables_that_bulk_copies_cannot_take(R):
     """Tables whose rows do not start on 16-byte boundaries, by R or by their address."""

@@ -21,7 +21,7 @@ def lib():
 
 def _page_plan(lib, **kw):
     a = dict(ctx=FAKE, new=FAKE, held=FAKE, held_out=OTHER, table=FAKE, ring=FAKE, state=FAKE, state_out=OTHER,
-             granted=FAKE, slots=FAKE, B=2, T=4, page=16, max_pages=4, num_pages=9)
+             granted=OTHER + 16, slots=OTHER + 32, B=2, T=4, page=16, max_pages=4, num_pages=9)
     a.update(kw)
     return lib.relbias_page_plan(*a.values(), None)
 
@@ -30,6 +30,7 @@ def _page_plan(lib, **kw):
     (dict(B=-1), ARG), (dict(T=-1), ARG), (dict(page=0), ARG), (dict(max_pages=0), ARG), (dict(num_pages=0), ARG),
     (dict(ctx=None), ARG), (dict(slots=None), ARG), (dict(ring=None), ARG), (dict(state=None), ARG),
     (dict(table=FAKE + 2), ARG), (dict(held_out=FAKE), ARG), (dict(state_out=FAKE), ARG),
+    (dict(slots=OTHER, granted=OTHER + 64, new=OTHER + 64), ARG), (dict(slots=OTHER + 64, ctx=OTHER + 64), ARG),
     (dict(num_pages=1 << 28), UNSUPPORTED), (dict(max_pages=1 << 28), UNSUPPORTED),
     (dict(T=(65535 * 2048) + 1), UNSUPPORTED), (dict(B=(1 << 31) - 1), UNSUPPORTED),
 ])
@@ -105,7 +106,8 @@ def _tree(lib, **kw):
     (dict(B=-1), ARG), (dict(Hq=7), ARG), (dict(R=-1), ARG), (dict(w=None), ARG), (dict(scale=0.0), ARG),
     (dict(dtype=5), ARG), (dict(dtype=ops.RELBIAS_FP32), UNSUPPORTED), (dict(T=129), UNSUPPORTED),
     (dict(d=96), UNSUPPORTED), (dict(Hq=34), UNSUPPORTED), (dict(page=24), ARG), (dict(max_ctx=129), ARG),
-    (dict(max_ctx=-1), ARG), (dict(q=None), ARG), (dict(mask=None), ARG), (dict(r=None), ARG), (dict(ws=None), ARG), (dict(ws=FAKE + 8), ARG),
+    (dict(max_ctx=-1), ARG), (dict(R=(1 << 30) + 1), UNSUPPORTED),
+    (dict(max_ctx=(1 << 30) + 1, max_pages=1 << 26, num_pages=1 << 20), UNSUPPORTED), (dict(q=None), ARG), (dict(mask=None), ARG), (dict(r=None), ARG), (dict(ws=None), ARG), (dict(ws=FAKE + 8), ARG),
     (dict(o=FAKE + 8), ARG), (dict(table=FAKE + 2), ARG), (dict(lse=FAKE + 1), ARG), (dict(B=65536), UNSUPPORTED)])
 def test_tree_attention_refuses(lib, kw, code):
     assert _tree(lib, **kw) == code
