@@ -592,9 +592,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     cut = make_int4(1 + (after + s.per - 1) / s.per, s.b, s.g, s.n);
                 }
                 for (int t = s.first_slice; t < s.ntiles; ++t, ++n) {
-                    const int buf = p.tab_bufs == 2 ? n & 1 : 0, use = p.tab_bufs == 2 ? n >> 1 : n;
-                    if (!(ok = tree_all(mbar_wait(&sh->tab_empty[buf], (use & 1) ^ 1, abort_flag)))) break;
-                    uint32_t* vis = reinterpret_cast<uint32_t*>(bufs + buf * buf_bytes);
+                    // Slice n signals on bars n % 2, phase n / 2, so that a slot meets one pair of bars in a
+                    // segment, every phase of them, with one buffer as with two.  The buffer is free
+                    // when slice n - 2, or with one buffer slice n - 1, has been read.
+                    const int buf = n & 1, last = n - p.tab_bufs;
+                    if (last >= 0 &&
+                        !(ok = tree_all(mbar_wait(&sh->tab_empty[last & 1], (last >> 1) & 1, abort_flag))))
+                        break;
+                    uint32_t* vis = reinterpret_cast<uint32_t*>(bufs + (p.tab_bufs == 2 ? buf : 0) * buf_bytes);
                     int* kpos = reinterpret_cast<int*>(vis + kMaxTree * 4);
                     float* tab = reinterpret_cast<float*>(kpos + kTrN);
                     const int j0 = s.jbase + t * kTrN;
@@ -651,10 +656,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // Drain the bulk copies.  After an abort the second warp may be a slice behind the first,
             // which issues them: it arrives in its place.
             if (!ok && lane == 0 && warp == kTrSoftmaxWarps + 3)
-                for (int x = 0; x < p.tab_bufs; ++x) mbar_arrive(&sh->tab_full[x]);
+                for (int x = 0; x < 2; ++x) mbar_arrive(&sh->tab_full[x]);
             if (p.w_bulk && warp == kTrSoftmaxWarps + 2)
-                for (int x = max(0, n - p.tab_bufs); x < n; ++x)
-                    mbar_drain_wait(&sh->tab_full[p.tab_bufs == 2 ? x & 1 : 0], (p.tab_bufs == 2 ? x >> 1 : x) & 1);
+                for (int x = max(0, n - 2); x < n; ++x) mbar_drain_wait(&sh->tab_full[x & 1], (x >> 1) & 1);
         }
     } else {
         // ---------------------------------------------------------------- softmax / epilogue
@@ -709,12 +713,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const int j0 = jbase + t * kTrN;
                 const bool slice = t >= first_slice;
                 const int n = nslice + t - first_slice;
-                const int buf = p.tab_bufs == 2 ? n & 1 : 0, use = p.tab_bufs == 2 ? n >> 1 : n;
-                const uint32_t* vis = reinterpret_cast<const uint32_t*>(bufs + buf * buf_bytes);
+                const int buf = n & 1;
+                const uint32_t* vis = reinterpret_cast<const uint32_t*>(bufs + (p.tab_bufs == 2 ? buf : 0) * buf_bytes);
                 const int* kpos = reinterpret_cast<const int*>(vis + kMaxTree * 4);
                 const float* tab = reinterpret_cast<const float*>(kpos + kTrN) + hh * tstride;
                 if (!(ok = tree_all(mbar_wait(&sh->s_full[slot], ns & 1, abort_flag)))) break;
-                if (slice && !(ok = tree_all(mbar_wait(&sh->tab_full[buf], use & 1, abort_flag)))) break;
+                if (slice && !(ok = tree_all(mbar_wait(&sh->tab_full[buf], (n >> 1) & 1, abort_flag)))) break;
                 tc_fence_after();
                 const int own0 = ctx - j0 - half * 64;         // this half's first column with a tree key
                 const int dlo = max(ctx - j0 - (kTrN - 1), 0) & ~3;   // the slice's first distance

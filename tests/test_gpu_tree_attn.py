@@ -245,6 +245,15 @@ def test_large_ragged_batches(B, T, Hq, Hkv, d, page, window, bound):
     check(x, max_ctx=bound or None, what="ragged")
 
 
+@pytest.mark.parametrize("ctxs,lens,T,G,window,R", [
+    ([700, 1500, 30], [8, 7, 8], 8, 16, 0, 999),       # one row tile, its key tiles shared by the slots
+    ([1500, 1200, 900], [8, 8, 8], 8, 14, 700, 1000),
+    ([700, 300, 1400], [5, 128, 9], 128, 16, 0, 1024),  # one row tile among sequences with many
+])
+def test_groups_whose_bias_slices_have_one_buffer(ctxs, lens, T, G, window, R):
+    check(make(ctxs, lens, T, G, 1, 128, 16, window, R, seed=G + T))
+
+
 def test_no_sequence_has_a_node():
     x = make([30, 0, 5000], [0, 0, 0], 8, 8, 2, 64, 16, 0, 16, seed=1)
     check(x)
