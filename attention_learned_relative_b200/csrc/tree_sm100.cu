@@ -58,6 +58,11 @@
 // and exchanged their maxima, for the weights.  The reference max of a row moves, and O is
 // rescaled, only when the max has grown by more than 2^8.
 //
+// Measured (ten calls in a graph): 8 nodes on 1,048,560 rows, 32 heads on 4 of 128, 331-349 us
+// (0.94-0.99 of the copy rate, HBM-bound); 64 nodes on eight caches of 73,728 to 131,072 rows
+// 870-1060 us (800-975 TFLOP/s, bound by each slot's chain); 16 nodes on 64 windows of 512
+// 32 us (start-up and the same chain); 4 nodes on a window of 64 9.5 us (cold loads in turn).
+//
 // Masks.  Sixteen-column chunks that hold tree keys are masked, and given their bias, by a
 // pass over S in tensor memory before the softmax reads it.  Other chunks add their bias in
 // registers, if any key is nearer than R, and are masked by one compare per key only in
@@ -192,10 +197,10 @@ struct TreeWalk {
         next_n = __ldg(p.tree_lens + x);
     }
     // Finds the start of run number `run`, by a whole warp: the stream's length, then the
-    // sequence that holds the run's first tile.
-    __device__ __forceinline__ void start(const TreeAttnParams& p, int grp, int npt, int run, int lane) {
+    // sequence that holds the run's first tile.  head: the lengths of sequence `lane`.
+    __device__ __forceinline__ void start(const TreeAttnParams& p, int grp, int npt, int run, int lane, int2 head) {
         auto tiles_of = [&](int x, TreeSeq& s) {
-            s = tree_seq(p, __ldg(p.ctx_lens + x), __ldg(p.tree_lens + x));
+            s = x < 32 ? tree_seq(p, head.x, head.y) : tree_seq(p, __ldg(p.ctx_lens + x), __ldg(p.tree_lens + x));
             if (s.bad && grp == 0 && run == 0) atomicOr(&g_status, kStatusBadLength);
             return 2 * grp * npt < s.n ? s.nt * p.Hkv : 0;
         };
@@ -361,6 +366,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const int tstride = tree_tab_stride(p.T), buf_bytes = tree_buf_bytes(p.G, p.T);
     volatile int* abort_flag = &sh->abort_flag;
 
+    // The schedule's first loads are under way while the bars are set up.
+    int2 head = make_int2(0, 0);
+    if (warp == 16 && lane < p.B) head = make_int2(__ldg(p.ctx_lens + lane), __ldg(p.tree_lens + lane));
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh->q_full[s], 1);
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const bool leader = elect_one();
             const int nboxes = kTrN / p.box_rows;
             TreeWalk walk;
-            walk.start(p, grp, npt, run, lane);
+            walk.start(p, grp, npt, run, lane, head);
             bool ok = true;
             int nk = 0, nv = 0, ks = 0, vs = 0, kph = 1, vph = 1;   // loads issued; next stages and their phases
             int nq[2] = {0, 0};                                     // loads of each Q buffer
@@ -894,13 +902,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 l = l * a_own + lo * a_other;
                 m = top;
             }
-            // Which slots' O hold something, and are waited for.
-            const bool own = two || ls == 0 || units > 1, other = !two && (ls == 1 || units > 1);
-            if (own && !(ok = tree_all(mbar_wait(&sh->o_final[slot], nf[slot] & 1, abort_flag)))) break;
-            if (other && !(ok = tree_all(mbar_wait(&sh->o_final[slot ^ 1], nf[slot ^ 1] & 1, abort_flag)))) break;
-            if (own) ++nf[slot];
-            if (two || ls == 1 || units > 1) ++nf[slot ^ 1];
-            tc_fence_after();
             const bool left = s.tile0 > 0, direct = !left && ntiles == s.nt;
             if (direct) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -917,6 +918,21 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                    (two ? ls * kTrM : 0) + ri) * (D + kTrRec);
             const uint32_t o_tm = tmem_base + lane_off + 256;
             const int part = two ? half : slot * 2 + half, width = two ? D / 2 : D / 4;
+            if (row_ok && part == 0) {
+                if (!direct) {
+                    *reinterpret_cast<float2*>(rec + D) = make_float2(m, l);
+                } else if (p.lse != nullptr) {
+                    p.lse[(static_cast<size_t>(s.b) * p.Hq + h) * p.T + t_node] =
+                        l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                }
+            }
+            // Which slots' O hold something, and are waited for.
+            const bool own = two || ls == 0 || units > 1, other = !two && (ls == 1 || units > 1);
+            if (own && !(ok = tree_all(mbar_wait(&sh->o_final[slot], nf[slot] & 1, abort_flag)))) break;
+            if (other && !(ok = tree_all(mbar_wait(&sh->o_final[slot ^ 1], nf[slot ^ 1] & 1, abort_flag)))) break;
+            if (own) ++nf[slot];
+            if (two || ls == 1 || units > 1) ++nf[slot ^ 1];
+            tc_fence_after();
 #pragma unroll 1
             for (int c = part * width; c < (part + 1) * width; c += 32) {
                 // 32 columns; of a one-row-tile segment at d 64 a thread has 16, and takes its
@@ -969,14 +985,6 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                                           (lane & 3) * 4) = u[e];
                         }
                     }
-                }
-            }
-            if (row_ok && part == 0) {
-                if (!direct) {
-                    *reinterpret_cast<float2*>(rec + D) = make_float2(m, l);
-                } else if (p.lse != nullptr) {
-                    p.lse[(static_cast<size_t>(s.b) * p.Hq + h) * p.T + t_node] =
-                        l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 }
             }
             nslice += ntiles - first_slice;
