@@ -216,7 +216,7 @@ struct TreeAttnParams {
     int part_rows;                   // rows of a partial
     int max_tiles;                   // key tiles of the longest segment there may be
     bool whole;                      // runs take the whole segments that start in them; none is cut
-    int nq, nk, nv, tab_bufs;        // Q buffers, K and V stages, buffers of the stagers (set at the launch)
+    int nk, nv, tab_bufs;            // K and V stages, buffers of the stagers (set at the launch)
     int num_pages, page_size, max_pages, max_ctx;
     // x / page_size = x * page_mul >> page_shift for 0 <= x < 2^31
     uint64_t page_mul;

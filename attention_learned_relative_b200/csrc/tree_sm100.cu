@@ -84,11 +84,9 @@ constexpr int kTrThreads = 640, kTrSoftmaxWarps = 16;
 // 640 threads launch with 96 registers each; the split gives the same total.
 constexpr int kTrSoftmaxRegs = 104, kTrOtherRegs = 64;
 constexpr float kTrGrow = 8.0f;            // log2 units: O is rescaled when a row's max grows by more
-constexpr int kTrMinTiles = 1;             // least key tiles of a CTA's run
 constexpr int kTrRec = 4;                  // floats of a partial record beyond its output: max, sum, pad
 constexpr int kTrMaxStages = 4;            // of K, and of V
-constexpr int kTrLongSegment = 32;         // key tiles of a segment that counts as long
-constexpr int kTrCutTiles = 6;             // what cutting segments costs, in key tiles
+constexpr int kTrCutTiles = 4;             // what cutting segments costs, in key tiles
 constexpr int kTrSegs = 4;                 // published segments
 
 template <int D>
@@ -137,23 +135,17 @@ __host__ __device__ constexpr int tree_buf_bytes(int G, int T) {
     return kMaxTree * 16 + kTrN * 4 + G * tree_tab_stride(T) * 4;
 }
 
-// Buffers and stages that fit: [Q tiles][K ring][V ring][shared][stager buffers].
+// Stages and buffers that fit: [2 Q tiles][K ring][V ring][shared][stager buffers].
 struct TreeSmem {
-    int nq, nk, nv, bufs, bytes;
+    int nk, nv, bufs, bytes;
 };
-TreeSmem tree_smem(int d, int G, int T, bool one_row_tile, bool long_segments) {
+TreeSmem tree_smem(int d, int G, int T) {
     const int tile = kTrM * d * 2, most = 232448 - 1024 - kTrSharedBytes;
-    TreeSmem x{2, 2, 2, 2, 0};
-    // With one row tile a second Q buffer hides the load of the next segment's queries, a
-    // third V stage more of the cache's latency: the latter pays where segments are long.
-    if (one_row_tile && long_segments) x.nq = 1;
-    if (4 * tile + x.nq * tile + 2 * tree_buf_bytes(G, T) > most) x.bufs = 1;
-    auto fits = [&](int nk, int nv) { return (x.nq + nk + nv) * tile + x.bufs * tree_buf_bytes(G, T) <= most; };
-    if (fits(2, 3)) x.nv = 3;
-    if (fits(3, 3)) x.nk = 3;
-    if (fits(4, 4)) x.nk = x.nv = 4;
+    TreeSmem x{2, 2, 2, 0};
+    if (6 * tile + 2 * tree_buf_bytes(G, T) > most) x.bufs = 1;
+    if (10 * tile + x.bufs * tree_buf_bytes(G, T) <= most) x.nk = x.nv = 4;   // d 64
     // One CTA per SM: each allocates all of tensor memory.
-    x.bytes = std::max((x.nq + x.nk + x.nv) * tile + kTrSharedBytes + x.bufs * tree_buf_bytes(G, T) + 1024, 120 * 1024);
+    x.bytes = std::max((2 + x.nk + x.nv) * tile + kTrSharedBytes + x.bufs * tree_buf_bytes(G, T) + 1024, 120 * 1024);
     return x;
 }
 
@@ -213,7 +205,7 @@ struct TreeWalk {
             total += t;
         }
         total = __reduce_add_sync(0xffffffffu, total);
-        per = max((total + p.runs - 1) / p.runs, kTrMinTiles);
+        per = max((total + p.runs - 1) / p.runs, 1);
         const long long at = static_cast<long long>(run) * per;
         pos = static_cast<int>(min(at, static_cast<long long>(total)));
         stop = min(total - pos, per) + pos;
@@ -359,7 +351,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* q_tiles = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* k_ring = q_tiles + p.nq * L::kTile;
+    uint8_t* k_ring = q_tiles + 2 * L::kTile;
     uint8_t* v_ring = k_ring + p.nk * L::kTile;
     TreeShared* sh = reinterpret_cast<TreeShared*>(v_ring + p.nv * L::kTile);
     uint8_t* bufs = reinterpret_cast<uint8_t*>(sh) + kTrSharedBytes;
@@ -477,10 +469,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 };
                 int page, prow, next_page, next_row;
                 lookup(0, next_page, next_row);
-                // Two row tiles go to buffers 0 and 1; single ones alternate where there are two, so
-                // that a segment's queries arrive while the one before is still being read.
+                // Two row tiles go to buffers 0 and 1; single ones alternate, so that a segment's queries
+                // arrive while the one before is still being read.
                 for (int r = 0; r < (s.two ? 2 : 1); ++r) {
-                    const int buf = s.two ? r : p.nq == 2 ? i & 1 : 0;
+                    const int buf = s.two ? r : i & 1;
                     if (!(ok = tree_all(mbar_wait(&sh->q_empty[buf], (nq[buf] & 1) ^ 1, abort_flag)))) break;
                     if (leader) {
                         mbar_arrive_expect_tx(&sh->q_full[buf], npt * p.G * 128 * (D / 64));
@@ -555,7 +547,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (ntiles == 0) break;
                 for (int u = 0; u < units; ++u) {
                     const uint32_t ls = u & 1, slot = ls ^ parity;
-                    const uint32_t buf = two ? ls : p.nq == 2 ? i & 1 : 0;
+                    const uint32_t buf = two ? ls : i & 1;
                     const bool opens = !two || ls == 0, closes = !two || ls == 1;
                     if (opens && !(ok = tree_all(mbar_wait(&sh->k_full[ks], k_phase, abort_flag)))) break;
                     if (u <= two) {   // the unit reads its row tile for the first time
@@ -1079,8 +1071,8 @@ __global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(cons
 template <int D>
 cudaError_t launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, TreeAttnParams p,
                         cudaStream_t stream) {
-    const TreeSmem sm = tree_smem(D, p.G, p.T, p.part_rows == kTrM, p.max_tiles >= kTrLongSegment);
-    p.nq = sm.nq, p.nk = sm.nk, p.nv = sm.nv, p.tab_bufs = sm.bufs;
+    const TreeSmem sm = tree_smem(D, p.G, p.T);
+    p.nk = sm.nk, p.nv = sm.nv, p.tab_bufs = sm.bufs;
     cudaError_t e =
         cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm.bytes);
     if (e != cudaSuccess) return e;
@@ -1116,7 +1108,7 @@ TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int windo
     x.groups = (row_tiles + 1) / 2;
     x.part_rows = row_tiles > 1 ? 2 * kTrM : kTrM;
     const long long tiles = static_cast<long long>(B) * Hkv * tree_max_tiles(T, max_ctx, window, kTrN);
-    x.runs = static_cast<int>(std::min<long long>(std::max(1, sms / x.groups), (tiles + kTrMinTiles - 1) / kTrMinTiles));
+    x.runs = static_cast<int>(std::min<long long>(std::max(1, sms / x.groups), tiles));
     const size_t ctas = static_cast<size_t>(x.runs) * x.groups;
     x.cut_bytes = (ctas * sizeof(int4) + 255) / 256 * 256;
     x.bytes = x.cut_bytes + ctas * 2 * x.part_rows * (d + kTrRec) * sizeof(float);
@@ -1126,7 +1118,9 @@ TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int windo
 // Whether runs take whole segments.  What cutting saves is the difference between the
 // longest run of whole segments and an even share of the tiles, at the most (segments of
 // the longest length); what it costs, partials and the combine kernel, is worth about
-// kTrCutTiles tiles (a local layer of 64 sequences, 5-6 tiles a segment: 45.8 us cut, 32.3 whole).
+// kTrCutTiles tiles.  Cut against whole, windows of 512 (5-6 tiles a segment, 4 key/value
+// heads): one sequence 13-14 us against 16-18, 8 sequences 22-23 against 17-19, 64 sequences
+// 46-49 against 32-35.
 bool tree_whole_segments(int B, int Hkv, int runs, int max_tiles) {
     const long long items = static_cast<long long>(B) * Hkv;
     return (items + runs - 1) / runs * max_tiles <= (items * max_tiles + runs - 1) / runs + kTrCutTiles;
