@@ -507,7 +507,10 @@ def _on(dev: int, fn, *args):
 
 def _call(fn, dev: int, *args):
     """fn(*args, stream) with device `dev` current, on that device's current stream."""
-    rc = _on(dev, fn, *args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        rc = _on(dev, fn, *args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != RELBIAS_OK:
         _check(rc)
 
@@ -551,7 +554,7 @@ def page_plan(ctx_lens, new_lens, num_blocks, block_table, free_ring, ring_state
     _dense(free_ring, "free_ring", dev, i32, (num_pages,))
     _dense(ring_state, "ring_state", dev, i32, (2,))
     if slots is None:
-        slots = ctx_lens.new_empty((B, T))
+        slots = ctx_lens.new_empty(B, T)
     else:
         _dense(slots, "slots", dev, i32, (B, T))
     if granted is None:
@@ -589,7 +592,7 @@ def tree_plan(parents, tree_lens, depth=None, mask=None):
     else:
         _dense(depth, "depth", dev, i32, (B, T))
     if mask is None:
-        mask = parents.new_empty((B, T, words))
+        mask = parents.new_empty(B, T, words)
     else:
         _dense(mask, "mask", dev, i32, (B, T, words))
     _call(lib().relbias_tree_plan, dev, parents.data_ptr(), tree_lens.data_ptr(), depth.data_ptr(),
@@ -601,19 +604,18 @@ def _token_stride(t, name: str, lead: tuple) -> int:
     """Elements between the tokens of t [*lead, heads, d], whose heads are dense and whose
     leading axes are evenly spaced (a slice of a projection's output, or dense)."""
     shape, st = t.shape, t.stride()
-    heads, d = shape[-2], shape[-1]
-    ok = shape[:-2] == lead and (d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d)
-    if len(lead) == 1:
-        step = st[0] if lead[0] > 1 else None
-    else:
-        step, span = None, 1
-        for i in range(len(lead) - 1, -1, -1):   # axes of one token have no say
-            if lead[i] > 1:
-                if step is None:
-                    step = st[i]
-                elif st[i] != step * span:
-                    ok = False
-            span *= lead[i]
+    heads, d = shape[-2:]
+    ok = shape[:-2] == lead and (st[-1] == 1 or d == 1) and (st[-2] == d or heads == 1)
+    if ok and len(lead) == 2 and lead[1] > 1 and (lead[0] == 1 or st[0] == lead[1] * st[1]):
+        return st[1]
+    step, span = None, 1
+    for i in range(len(lead) - 1, -1, -1):   # axes of one token have no say
+        if lead[i] > 1:
+            if step is None:
+                step = st[i]
+            elif st[i] != step * span:
+                ok = False
+        span *= lead[i]
     if not ok:
         raise ValueError("%s must be [%s, heads, d] with dense heads and evenly spaced tokens" % (name, lead))
     return heads * d if step is None else step
