@@ -237,13 +237,15 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const TreePlanParam
 // q'[c] = q[c] * wq[c] / sqrt(mean_c q[c]^2 + eps), the same for k with wk, both over one
 // head's d elements, the sum of squares in fp32; rows of k' and v go to cache row
 // slots[token].  One pass: every element is read once and written once, so the call is
-// bounded by HBM.  A head row is held by LANES threads, 16 bytes each (two vectors each
-// for 256 fp32 elements); blocks are persistent, so that a thread loads the weights of its
-// columns once.  Few rows in flight per thread and many threads did best: two 8192-token
-// prompts (336 MB) take 64.7 us (5.19 TB/s, 0.79 of the measured copy rate) with two rows and
-// six blocks per SM, 66.3 with four and four, 106.8 with eight and two.
+// bounded by HBM.  A head row is held by LANES threads, two 16-byte vectors each, so that
+// the addresses and the sum's exchange are worked out once for both; the weights lie in
+// shared memory, blocks are persistent.  Two 8192-token prompts (336 MB) take 54.5 us
+// (6.16 TB/s, 0.94 of the measured copy rate) with two rows in flight per thread and four
+// blocks per SM; 59.0-61.2 with two rows and three, five or six blocks, 59.6-63.2 with one
+// row, 55.1-64.7 with three or four.  One vector per thread with its weights in registers
+// (64.7 us) was bound by the instructions around each vector (issue slots 65% busy).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 2, kAppendBlocks = 6;   // rows in flight per thread, blocks per SM
+constexpr int kAppendRows = 2, kAppendBlocks = 4;   // rows in flight per thread, blocks per SM
 
 template <typename T>
 struct Vec;   // 16 bytes of T as pairs of floats
@@ -284,24 +286,19 @@ struct Vec<__nv_bfloat16> {
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kernel(const KvAppendParams p) {
     constexpr int N = Vec<T>::N;
-    constexpr int kVecs = D / N;                       // 16-byte vectors of a head row
-    constexpr int LANES = kVecs < 32 ? kVecs : 32;     // threads of a head row
-    constexpr int VPL = kVecs / LANES;                 // vectors of a thread
+    constexpr int VPL = 2;                             // 16-byte vectors of a thread
+    constexpr int LANES = D / N / VPL;                 // threads of a head row
     constexpr int kRows = kAppendThreads / LANES;      // rows of a block and pass
-    constexpr int kFlight = VPL == 1 ? kAppendRows : 2;
+    constexpr int kFlight = kAppendRows;
+    __shared__ __align__(16) float weights[2][D];      // of queries and keys
     const int sub = threadIdx.x % LANES;
     const unsigned heads = static_cast<unsigned>(p.heads_q + 2 * p.Hkv);
     const unsigned rows = static_cast<unsigned>(p.ntok) * heads;
-    // A thread's columns are the same in every row: their weights stay in registers.
-    uint64_t wq[VPL][N / 2], wk[VPL][N / 2];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v)
-#pragma unroll
-        for (int e = 0; e < N / 2; ++e) {
-            const int c = (v * LANES + sub) * N + 2 * e;
-            wq[v][e] = p.q_weight != nullptr ? f2_pack(__ldg(p.q_weight + c), __ldg(p.q_weight + c + 1)) : 0;
-            wk[v][e] = p.k_weight != nullptr ? f2_pack(__ldg(p.k_weight + c), __ldg(p.k_weight + c + 1)) : 0;
-        }
+    for (int c = threadIdx.x; c < D; c += kAppendThreads) {
+        weights[0][c] = p.q_weight != nullptr ? __ldg(p.q_weight + c) : 0.0f;
+        weights[1][c] = p.k_weight != nullptr ? __ldg(p.k_weight + c) : 0.0f;
+    }
+    __syncthreads();
     for (unsigned r0 = blockIdx.x * static_cast<unsigned>(kRows * kFlight); r0 < rows;
          r0 += gridDim.x * static_cast<unsigned>(kRows * kFlight)) {
         uint4 x[kFlight][VPL];
@@ -353,9 +350,13 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
                 const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
                 for (int v = 0; v < VPL; ++v) {
+                    const float4* w = reinterpret_cast<const float4*>(&weights[kind[u]][(v * LANES + sub) * N]);
 #pragma unroll
-                    for (int e = 0; e < N / 2; ++e)
-                        f[v][e] = f2_mul(f2_mul(f[v][e], inv2), kind[u] == 0 ? wq[v][e] : wk[v][e]);
+                    for (int e = 0; e < N / 2; e += 2) {
+                        const float4 w4 = w[e / 2];
+                        f[v][e] = f2_mul(f2_mul(f[v][e], inv2), f2_pack(w4.x, w4.y));
+                        f[v][e + 1] = f2_mul(f2_mul(f[v][e + 1], inv2), f2_pack(w4.z, w4.w));
+                    }
                     x[u][v] = Vec<T>::pack(f[v]);
                 }
             }
@@ -430,8 +431,7 @@ __global__ void __launch_bounds__(128) kv_compact_kernel(const KvCompactParams p
 
 template <typename T, int D>
 cudaError_t launch_append(const KvAppendParams& p, int sms, cudaStream_t stream) {
-    constexpr int vecs = D / Vec<T>::N;
-    constexpr int per = kAppendThreads / (vecs < 32 ? vecs : 32) * (vecs <= 32 ? kAppendRows : 2);
+    constexpr int per = kAppendThreads / (D / Vec<T>::N / 2) * kAppendRows;   // rows of a block and pass
     const long long rows = static_cast<long long>(p.ntok) * (p.heads_q + 2 * p.Hkv);
     const int grid = static_cast<int>(std::min<long long>((rows + per - 1) / per, static_cast<long long>(kAppendBlocks) * sms));
     kv_append_kernel<T, D><<<grid, kAppendThreads, 0, stream>>>(p);
