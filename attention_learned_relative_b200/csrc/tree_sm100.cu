@@ -337,6 +337,13 @@ __device__ __forceinline__ void tree_transpose4(uint4 (&u)[4], int lane) {
             }
 }
 
+// Log-sum-exp of a row from its reference max (log2 units) and the sum against it.  A row
+// that sees nothing has a sum of 0.  A NaN or +inf logit leaves the max as it was, or at
+// +inf, but makes the sum NaN, and the log-sum-exp with it.
+__device__ __forceinline__ float tree_lse(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 __device__ __forceinline__ bool tree_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 template <int D>
@@ -914,8 +921,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (!direct) {
                     *reinterpret_cast<float2*>(rec + D) = make_float2(m, l);
                 } else if (p.lse != nullptr) {
-                    p.lse[(static_cast<size_t>(s.b) * p.Hq + h) * p.T + t_node] =
-                        l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[(static_cast<size_t>(s.b) * p.Hq + h) * p.T + t_node] = tree_lse(m, l);
                 }
             }
             // Which slots' O hold something, and are waited for.
@@ -1021,20 +1027,21 @@ __global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(cons
 #pragma unroll
         for (int e = 0; e < E; e += 2)
             ahead[s][e / 2] = s < cut.x ? *reinterpret_cast<const float2*>(rec(s) + lane * E + e) : make_float2(0.f, 0.f);
-    // Lane x holds the max and sum of parts x, x + 32, ... merged.
+    // Lane x holds the max and sum of parts x, x + 32, ... merged.  A part whose logits are all
+    // NaN has a max of -inf and a sum of NaN, which the total keeps.
     float m = -INFINITY, l = 0.0f, m_own = -INFINITY;
     for (int s = lane; s < cut.x; s += 32) {
         const float2 ml = *reinterpret_cast<const float2*>(rec(s) + D);
         const float top = fmaxf(m, ml.x);
         const float a = m == -INFINITY ? 0.0f : ex2_approx(m - top);
-        l = l * a + (ml.x == -INFINITY ? 0.0f : ml.y * ex2_approx(ml.x - top));
+        l = l * a + (ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - top));
         m = top;
         if (s == lane) m_own = ml.x;
     }
     float M = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    l = m == -INFINITY ? 0.0f : l * ex2_approx(m - M);
+    if (m != -INFINITY) l *= ex2_approx(m - M);   // else 0, or NaN
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float w_own = m_own == -INFINITY ? 0.0f : ex2_approx(m_own - M);
@@ -1065,7 +1072,7 @@ __global__ void __launch_bounds__(kTrCombineWarps * 32) tree_combine_kernel(cons
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
     if (p.lse != nullptr && lane == 0)
-        p.lse[(static_cast<size_t>(cut.y) * p.Hq + h) * p.T + t] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
+        p.lse[(static_cast<size_t>(cut.y) * p.Hq + h) * p.T + t] = tree_lse(M, l);
 }
 
 template <int D>

@@ -463,7 +463,7 @@ RELBIAS_API int relbias_kv_append(const void* q, const void* k, const void* v, c
  *     mask as relbias_tree_plan writes them, or any other mask
  *   max_ctx_len bounds every ctx_lens[b] and plans the key splits.
  * Rows t >= tree_lens[b] of o and lse are left as they were.  A node that sees nothing gets
- * o = 0 and lse = -inf.  Cache rows that no node of a sequence sees by position (past its
+ * o = 0 and lse = -inf; one that sees a NaN or +inf logit gets NaN in both.  Cache rows that no node of a sequence sees by position (past its
  * tree, or before the window of its first node) may hold anything; the values of rows
  * inside that range must be finite, those of masked nodes included.
  * T <= 128; page_size a multiple of 16; Hq / Hkv <= 16; bf16, d in {64, 128}; max_ctx_len and
