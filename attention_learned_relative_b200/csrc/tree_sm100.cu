@@ -691,7 +691,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             row.ok = node < npt && row.t < s.n;
             const size_t at = static_cast<size_t>(s.b) * p.T + (row.ok ? row.t : 0);
             row.dep = __ldg(p.depth + at);
-            row.r = row.ok ? __ldg(p.r + at * p.Hq + s.g * p.G + hh) : 0.0f;
+            // Without a table r has no say, whatever it holds (tiles with tree keys multiply it by 0).
+            row.r = row.ok && p.R > 0 ? __ldg(p.r + at * p.Hq + s.g * p.G + hh) : 0.0f;
         };
         if ((ok = seg_wait(0)) && sh->segs[0].ntiles > 0) load_row(sh->segs[0], slot);
         for (int i = 0; ok; ++i) {

@@ -462,6 +462,7 @@ RELBIAS_API int relbias_kv_append(const void* q, const void* k, const void* v, c
  *   ctx_lens, tree_lens [B], depth [B, T], mask [B, T, ceil(T / 32)]: int32, device; depth and
  *     mask as relbias_tree_plan writes them, or any other mask
  *   max_ctx_len bounds every ctx_lens[b] and plans the key splits.
+ *   r must be finite (distances of R or more multiply it by 0); with R = 0 it is not read.
  * Rows t >= tree_lens[b] of o and lse are left as they were.  A node that sees nothing gets
  * o = 0 and lse = -inf; one that sees a NaN or +inf logit gets NaN in both.  Cache rows that no node of a sequence sees by position (past its
  * tree, or before the window of its first node) may hold anything; the values of rows

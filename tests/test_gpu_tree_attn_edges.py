@@ -99,3 +99,14 @@ def test_infinite_logits(ctxs, lens, T, Hq, Hkv, d, page, window):
         assert (x["q"][0, s, :, 3] != 0).all()
         assert torch.isnan(out[0, s, up].float()).all() and torch.isnan(lse[0, up, s]).all()
         assert torch.isfinite(out[0, s, ~up].float()).all() and torch.isfinite(lse[0, ~up, s]).all()
+
+
+def test_without_a_table_r_has_no_say():
+    """R = 0: there is no bias, whatever r holds, as in the decode step."""
+    for value in (float("nan"), float("inf"), -float("inf")):
+        x = make([513, 40], [7, 9], 9, 6, 2, 64, 16, 0, 0, seed=4)
+        x["r"].zero_()
+        want, want_lse = call(x, 0.125)
+        x["r"].fill_(value)
+        out, lse = call(x, 0.125)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
