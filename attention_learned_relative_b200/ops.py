@@ -521,8 +521,8 @@ def _on_stream(fn):
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
-        first = args[0] if args else next(iter(kw.values()))
-        if first.get_device() != stream.device.index:
+        first = next((x for x in (*args, *kw.values()) if isinstance(x, torch.Tensor)), None)
+        if first is not None and first.get_device() != stream.device.index:
             raise ValueError("the stream is not on the tensors' device")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)

@@ -110,3 +110,14 @@ def test_without_a_table_r_has_no_say():
         x["r"].fill_(value)
         out, lse = call(x, 0.125)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_a_stream_with_all_arguments_by_keyword():
+    side = torch.cuda.Stream()
+    parents = torch.tensor([[-1, 0, 0, 1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([4], dtype=torch.int32, device="cuda")
+    want = ops.tree_plan(parents, lens)
+    side.wait_stream(torch.cuda.current_stream())
+    got = ops.tree_plan(depth=None, mask=None, parents=parents, tree_lens=lens, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
