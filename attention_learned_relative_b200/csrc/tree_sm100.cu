@@ -19,11 +19,12 @@
 //
 // Schedule.  Sequence lengths are known on the device only, and a batch is ragged.  The
 // key tiles of all (sequence, key/value head) segments form one stream, and each CTA takes
-// an equal run of it: every CTA works for the same time whatever the lengths, in one wave.
+// an equal run of it: as many key tiles as any other whatever the lengths, in one wave.
 // A run covers the end of one segment, whole segments, and the start of another; whole
 // segments are written out directly, the two cut ones as partials (unnormalised output,
-// max, sum) that the combine kernel merges.  Where segments are short and many, a run takes
-// the whole segments that start in it instead: nothing is cut, and nothing combined.  CTAs
+// max, sum) that the combine kernel merges.  Where segments are many and none can be long
+// (tree_whole_segments), a run takes the whole segments that start in it instead: nothing
+// is cut, and nothing combined, and a run exceeds its share by less than a segment.  CTAs
 // of different row pairs run the same stream side by side, so a K/V tile comes from HBM
 // once and from L2 for the others.
 //
@@ -87,6 +88,7 @@ constexpr float kTrGrow = 8.0f;            // log2 units: O is rescaled when a r
 constexpr int kTrRec = 4;                  // floats of a partial record beyond its output: max, sum, pad
 constexpr int kTrMaxStages = 4;            // of K, and of V
 constexpr int kTrCutTiles = 4;             // what cutting segments costs, in key tiles
+constexpr int kTrWholeTiles = 12;          // the longest segment that is never cut, in key tiles
 constexpr int kTrSegs = 4;                 // published segments
 
 template <int D>
@@ -1123,15 +1125,23 @@ TreeLaunch tree_launch_plan(int B, int T, int Hkv, int G, int max_ctx, int windo
     return x;
 }
 
-// Whether runs take whole segments.  What cutting saves is the difference between the
-// longest run of whole segments and an even share of the tiles, at the most (segments of
-// the longest length); what it costs, partials and the combine kernel, is worth about
-// kTrCutTiles tiles.  Cut against whole, windows of 512 (5-6 tiles a segment, 4 key/value
-// heads): one sequence 13-14 us against 16-18, 8 sequences 22-23 against 17-19, 64 sequences
-// 46-49 against 32-35.
+// Whether runs take whole segments.  If all segments are as long as the longest may be,
+// whole runs differ from an even share by the rounding of items / runs to whole segments;
+// cutting costs partials and the combine kernel, worth about kTrCutTiles tiles.  Lengths are
+// known on the device only, though: if one segment is long and the others short, the share
+// shrinks and the run that holds the long one does not, so the longest possible segment is
+// bounded too.  Cut against whole (us; 16 nodes, 4 key/value heads of 128, 148 runs):
+//   longest (tiles)                    6            12           16           32           64
+//   37 sequences of that length        23.0  19.5   34.2  30.2   42.1  37.8   69.3  64.7    110  107
+//   lengths falling evenly to 0        28.7  24.5   47.2  34.3   53.1  44.5   70.7  54.3   95.1 88.4
+//   one, the others of 100 rows        21.3  19.5   20.6  26.1   20.3  30.3   21.7  47.2   28.7 81.4
+// and windows of 512 (5-6 tiles): one sequence 13.6 against 17.1, 8 sequences 23.0 against 18.4,
+// 64 sequences 45.8 against 32.6.  A bound of 12 tiles makes the loss on the worst of these
+// batches the smallest: 27% at 12 (one long segment), 30% at 32 (falling lengths, cut).
 bool tree_whole_segments(int B, int Hkv, int runs, int max_tiles) {
     const long long items = static_cast<long long>(B) * Hkv;
-    return (items + runs - 1) / runs * max_tiles <= (items * max_tiles + runs - 1) / runs + kTrCutTiles;
+    return max_tiles <= kTrWholeTiles &&
+           (items + runs - 1) / runs * max_tiles <= (items * max_tiles + runs - 1) / runs + kTrCutTiles;
 }
 
 cudaError_t launch_tree_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
