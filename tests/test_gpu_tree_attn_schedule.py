@@ -58,3 +58,30 @@ def test_a_long_sequence_is_shared_out_whatever_the_batch():
     even = [sum(ragged) // B] * B
     t_ragged, t_even = _time(ragged, 16, 32, Hkv, 128, 64), _time(even, 16, 32, Hkv, 128, 64)
     assert t_ragged <= 3 * t_even, (t_ragged, t_even)
+
+
+@pytest.mark.parametrize("R,temp_n0", [(32, 0), (12000, 500)])
+def test_more_parts_than_a_warp_has_lanes(R, temp_n0):
+    """One cache head of 12000 rows is a key tile to a CTA: 94 parts, so that a lane of the
+    combine merges several, with the bias near the end only and over all parts."""
+    ops.device_status(reset=True)
+    for T in (2, 70):   # one row tile, and two
+        check(make([12000], [T], T, 2, 1, 64, 64, 0, R, seed=R), temp_n0=temp_n0, what="94 parts")
+    assert ops.device_status(reset=True) == 0
+
+
+def test_a_sequence_alone_and_in_a_batch():
+    """Where segments are cut depends on the batch, so bits may differ; both answers are within
+    the bound of the exact one."""
+    ops.device_status(reset=True)
+    args = (16, 32, 4, 128, 32)
+    ctxs, lens = [900, 200, 31], [16, 9, 16]
+    for window in (0, 100):
+        x = make(ctxs, lens, *args, window, 128, seed=3)
+        check(x, what="batch")
+        for b in range(3):
+            y = dict(x, ctxs=ctxs[b:b + 1], lens=lens[b:b + 1], q=x["q"][b:b + 1].contiguous(),
+                     r=x["r"][b:b + 1].contiguous(), table=x["table"][b:b + 1].contiguous(), ks=x["ks"][b:b + 1],
+                     vs=x["vs"][b:b + 1], depth=x["depth"][b:b + 1], anc=x["anc"][b:b + 1])
+            check(y, what="alone")
+    assert ops.device_status(reset=True) == 0
