@@ -32,8 +32,10 @@ namespace {
 // (B ints from L2) and the whole plan is one launch.
 //
 // Bounded by the launch and two dependent L2 round trips for small batches (64 requests of
-// 16 rows: 3.5 us in a graph), and by the slot map for long prompts (256 requests of up to
-// 8192 rows, 8.4 MB of slots: 8.4 us, 1.0 TB/s).
+// 16 rows: 3.4-3.8 us in a graph).  For long prompts (256 requests of up to 8192 rows, 8.4 MB of
+// slots: 8.2-8.4 us, 1.0 TB/s) the slot loop leads: a thread's eight slots are 4-byte steps of a
+// division, a table read and a store, one after the other, since the table may alias the slots
+// for all the compiler knows.
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanSlots = 8 * kPlanThreads;   // slots a block writes
@@ -239,8 +241,8 @@ __global__ void __launch_bounds__(kMaxTree) tree_plan_kernel(const TreePlanParam
 // slots[token].  One pass: every element is read once and written once, so the call is
 // bounded by HBM.  A head row is held by LANES threads, two 16-byte vectors each, so that
 // the addresses and the sum's exchange are worked out once for both; the weights lie in
-// shared memory, blocks are persistent.  Two 8192-token prompts (336 MB) take 54.5 us
-// (6.16 TB/s, 0.94 of the measured copy rate) with two rows in flight per thread and four
+// shared memory, blocks are persistent.  Two 8192-token prompts (336 MB) take 54.5-55.4 us
+// (6.06-6.16 TB/s, 0.92-0.94 of the measured copy rate) with two rows in flight per thread and four
 // blocks per SM; 59.0-61.2 with two rows and three, five or six blocks, 59.6-63.2 with one
 // row, 55.1-64.7 with three or four.  One vector per thread with its weights in registers
 // (64.7 us) was bound by the instructions around each vector (issue slots 65% busy).
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) kv_append_kerne
 // read before any move writes it.  A thread owns 16 bytes of the rows and moves them in
 // that order, kCompactBatch rows in flight: the rows a batch writes (i .. i + 7) lie below
 // every row a later batch reads.  No thread reads what another writes.  One launch for all
-// layers: 64 requests in 32 layers (29 MB) take 7.6-9.1 us, 8 requests in one 3.4-3.9 us.
+// layers: 64 requests in 32 layers (29 MB) take 7.6-9.3 us, 8 requests in one 3.4-3.9 us.
 
 constexpr int kCompactBatch = 8;
 

@@ -59,10 +59,13 @@
 // and exchanged their maxima, for the weights.  The reference max of a row moves, and O is
 // rescaled, only when the max has grown by more than 2^8.
 //
-// Measured (ten calls in a graph): 8 nodes on 1,048,560 rows, 32 heads on 4 of 128, 331-349 us
-// (0.94-0.99 of the copy rate, HBM-bound); 64 nodes on eight caches of 73,728 to 131,072 rows
-// 870-1060 us (800-975 TFLOP/s, bound by each slot's chain); 16 nodes on 64 windows of 512
-// 32 us (start-up and the same chain); 4 nodes on a window of 64 9.5 us (cold loads in turn).
+// Measured, ten calls in a graph (a few milliseconds), and in brackets trains of fifty, calls or
+// replays alike, in which the power cap takes the SM clock from 1965 to 1365-1515 MHz:
+// 8 nodes on 1,048,560 rows, 32 heads on 4 of 128, 330-350 us, 0.94-0.99 of the copy rate, HBM-bound
+// (360-430, 0.76-0.91); 64 nodes on eight caches of 73,728 to 131,072 rows 804-970 us, 874-1054
+// TFLOP/s (950-970), bound by each slot's chain and the issue of its products; 16 nodes on 64
+// windows of 512 32 us (start-up and the same chain); 4 nodes on a window of 64 9.5-9.9 us (cold
+// loads in turn).
 //
 // Masks.  Sixteen-column chunks that hold tree keys are masked, and given their bias, by a
 // pass over S in tensor memory before the softmax reads it.  Other chunks add their bias in
